@@ -325,6 +325,107 @@ int qgemm(const float *X, int64_t m, const woq_weight *w, float *Y, int32_t path
 int qgemm_bf16_noalloc(const float *X, int64_t m, const woq_weight *w, float *Y, void *stream);
 
 /*
+ * Attention: what a decoder layer does between its packed projections. A 4-bit cache of keys and
+ * values (kv4_append, kv4_gather) and one-token attention over it (kv4_attn).
+ *
+ * Activations are float32 as everywhere in this library; these calls also take binary16 and
+ * bfloat16 ones. Whatever the type, scores, softmax and sums are FP32.
+ */
+#define WOQ_F32  0
+#define WOQ_F16  1
+#define WOQ_BF16 2
+
+/*
+ * Rows of heads in device memory: element (t, h, d) is at data + t * row_stride +
+ * h * head_stride + d, strides in elements. A slice of a fused projection's output [t, q | k | v]
+ * is such an array. data is 16-byte aligned and both strides are positive multiples of 16 bytes;
+ * head_stride is at least the heads' dim.
+ */
+typedef struct woq_rows {
+  void *data;
+  int32_t dtype;       /* WOQ_F32, WOQ_F16 or WOQ_BF16 */
+  int32_t heads;
+  int64_t row_stride;
+  int64_t head_stride;
+} woq_rows;
+
+/*
+ * A paged cache of keys and values, int4 in blocks of 32 along dim (q4b32, as the weights), 4.5
+ * bits an element. A page holds `page` consecutive tokens of one sequence for every key head.
+ *   codes   device, 64-byte aligned, [pages, kv_heads, 2 (key, value), page, dim / 2] bytes
+ *   scales  device, 64-byte aligned, [pages, kv_heads, page, 2 (key, value), dim / 32] binary16
+ *   dim     64 or 128;  page a power of two, 16 to 65536;  kv_heads 1 to 1024;  pages < 2^31
+ * A row's blocks are packed as an int4 weight's, and its pieces then reordered for the attention
+ * kernel: of a key row, 32-bit word t of block b is kept at word t * (dim / 32) + b; of a value row,
+ * 16-bit halfword g of block b at halfword g * (dim / 32) + b. kv4_gather reads it back.
+ */
+typedef struct woq_kv4 {
+  uint8_t *codes;
+  uint16_t *scales;
+  int64_t pages;
+  int32_t kv_heads;
+  int32_t dim;
+  int32_t page;
+} woq_kv4;
+
+/*
+ * kv4_append -- quantises key and value rows into the cache with qpack's int4 arithmetic, bit for
+ * bit: scale = binary16(max|x| / 7), code = clamp(round-half-even(x / scale), -8, 7). A block that
+ * holds a NaN, or whose scale overflows binary16, reads back as NaN.
+ * Rows are packed sequence after sequence: row t of sequence b, cu[b] <= t < cu[b + 1], becomes token
+ * start[b] + t - cu[b] of it, which lives in page table[b, token / page].
+ *   k, v    device, [tokens, kv_heads, dim], any of the three types
+ *   cu      device, int32 [batch + 1], non-decreasing; rows before cu[0] and from cu[batch] on are
+ *           not touched (nor read)
+ *   start   device, int32 [batch]: tokens that each sequence has already; NULL for none
+ *   table   device, int32 [batch, width] row-major
+ * The lengths stay on the device, so that a captured call follows them. A row whose token has no
+ * page (a token beyond width * page, a negative start, or an entry outside [0, pages)) is
+ * dropped. Two rows of one call must not fall on the same token of the same page.
+ * batch 1 to 4096, width 1 to 2^31 - 1; tokens == 0 does nothing.
+ * Errors: WOQ_EINVAL (null pointers, dtype, batch, page, heads of k or v), WOQ_ESHAPE (dim, sizes,
+ * strides), WOQ_EALIGN, WOQ_EDEVICE, WOQ_ECUDA.
+ */
+int kv4_append(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+               const int32_t *start, int32_t batch, const int32_t *table, int64_t width, void *stream);
+
+/*
+ * kv4_gather -- reads rows of the cache back, scale * code, addressed as kv4_append addresses them
+ * (a float32 result is exact; 16-bit ones are rounded once). A row of a sequence whose token has no
+ * page becomes 0; rows outside the sequences are left as they are. Arguments and errors as
+ * kv4_append, with k and v written.
+ */
+int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, int32_t batch, const int32_t *table,
+               int64_t width, int64_t tokens, const woq_rows *k, const woq_rows *v, void *stream);
+
+/*
+ * kv4_attn -- a decode step's attention: for each sequence b and query head h, with key head
+ * h / (q.heads / kv_heads), o[b, h] = sum_j p_j v_j over the sequence's lens[b] cached tokens,
+ * p = softmax_j(scale * q[b, h] . k_j). FP32 accuracy: the codes are exact, q and p enter the
+ * tensor cores with 22 significant bits, and each block's FP32 sum is scaled once.
+ * Deterministic for the same arguments on the same device.
+ *   q       device, [batch, q.heads, dim]; q.heads a multiple of kv_heads, at most 64 a key head
+ *   lens    device, int32 [batch]: cached tokens, the new one among them if it attends to itself.
+ *           0 or less gives a zero row; more than width * page counts as that
+ *   table   device, int32 [batch, width]; tokens in a page outside [0, pages) are not there, and
+ *           a sequence with no other tokens gives a zero row
+ *   scale   positive and finite, usually dim^-1/2
+ *   o       device, as q, of q's type, not overlapping q; fully written
+ *   workspace  device, 256-byte aligned, at least kv4_attn_workspace_bytes. It must be zero before
+ *           the first call, and every call leaves its counters zero (after a WOQ_ETIMEOUT from
+ *           woq_device_status, zero it before reuse); its size goes by batch and heads, not by
+ *           lengths. Calls (captured ones too) that share a workspace must be ordered on one stream.
+ * batch 1 to 4096. One launch whose grid does not depend on the lengths. Non-finite values in q, or in a
+ * block of a token that is attended to, make the results they enter NaN; nothing else of the
+ * cache's pages, such as slots behind the last token, has an influence.
+ * Errors: as kv4_append, WOQ_EINVAL for scale and an o that overlaps q, WOQ_EWORKSPACE.
+ */
+size_t kv4_attn_workspace_bytes(const woq_kv4 *cache, int32_t q_heads, int32_t batch);
+int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32_t batch, const int32_t *table,
+             int64_t width, float scale, const woq_rows *o, void *workspace, size_t workspace_bytes,
+             void *stream);
+
+/*
  * woq_device_status -- synchronises the current device, then returns WOQ_ETIMEOUT if any
  * kernel of this library recorded a bounded wait that gave up since the last call with
  * clear != 0 (and clears the record if clear != 0), WOQ_ECUDA if synchronisation failed,

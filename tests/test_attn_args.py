@@ -1,0 +1,117 @@
+"""Refusals of the attention calls, on the CPU: nothing here reaches a device."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import weight_only_bit_qgemv_b200 as woq
+from weight_only_bit_qgemv_b200 import _lib
+
+OK = 1 << 20  # an address that no call below dereferences
+FAR = 1 << 40
+
+
+def rows(data=OK, dtype=0, heads=2, row=256, head=128):
+    return _lib.WoqRows(data, dtype, heads, row, head)
+
+
+def kv4(codes=FAR, scales=2 * FAR, pages=4, heads=2, dim=128, page=16):
+    return _lib.WoqKv4(codes, scales, pages, heads, dim, page)
+
+
+BAD_CACHES = [
+    (kv4(codes=0), _lib.WOQ_EINVAL), (kv4(scales=0), _lib.WOQ_EINVAL),
+    (kv4(page=8), _lib.WOQ_EINVAL), (kv4(page=48), _lib.WOQ_EINVAL), (kv4(page=131072), _lib.WOQ_EINVAL),
+    (kv4(dim=96), _lib.WOQ_ESHAPE), (kv4(dim=256), _lib.WOQ_ESHAPE), (kv4(pages=0), _lib.WOQ_ESHAPE),
+    (kv4(pages=2**31), _lib.WOQ_ESHAPE), (kv4(heads=0), _lib.WOQ_ESHAPE), (kv4(heads=1025), _lib.WOQ_ESHAPE),
+    (kv4(codes=FAR + 32), _lib.WOQ_EALIGN), (kv4(scales=FAR + 2), _lib.WOQ_EALIGN),
+]
+BAD_ROWS = [
+    (rows(data=0), _lib.WOQ_EINVAL), (rows(dtype=3), _lib.WOQ_EINVAL), (rows(dtype=-1), _lib.WOQ_EINVAL),
+    (rows(row=0), _lib.WOQ_ESHAPE), (rows(row=-256), _lib.WOQ_ESHAPE), (rows(row=258), _lib.WOQ_ESHAPE),
+    (rows(dtype=1, row=260), _lib.WOQ_ESHAPE), (rows(head=64), _lib.WOQ_ESHAPE), (rows(row=2**40), _lib.WOQ_ESHAPE),
+    (rows(data=OK + 8), _lib.WOQ_EALIGN),
+]
+
+
+def test_step_refusals():
+    L = _lib.lib()
+
+    def both(c=None, k=None, v=None, tokens=4, cu=OK, start=None, batch=1, table=OK, width=1):
+        c, k, v = c or kv4(), k or rows(), v or rows(data=FAR)
+        a = L.kv4_append(ctypes.byref(c), ctypes.byref(k), ctypes.byref(v), tokens, cu, start, batch, table, width, None)
+        b = L.kv4_gather(ctypes.byref(c), cu, start, batch, table, width, tokens, ctypes.byref(k), ctypes.byref(v), None)
+        assert a == b
+        return a
+
+    for c, want in BAD_CACHES:
+        assert both(c=c) == want
+    for r, want in BAD_ROWS + [(rows(heads=3), _lib.WOQ_EINVAL)]:
+        assert both(k=r) == want and both(v=r) == want
+    assert both(tokens=-1) == _lib.WOQ_EINVAL and both(tokens=2**31) == _lib.WOQ_ESHAPE
+    assert both(cu=None) == _lib.WOQ_EINVAL and both(table=None) == _lib.WOQ_EINVAL
+    assert both(cu=OK + 2) == both(start=OK + 1) == both(table=OK + 2) == _lib.WOQ_EALIGN
+    assert both(batch=0) == both(batch=4097) == _lib.WOQ_EINVAL
+    assert both(width=0) == both(width=2**31) == _lib.WOQ_ESHAPE
+    assert L.kv4_append(None, ctypes.byref(rows()), ctypes.byref(rows()), 1, OK, None, 1, OK, 1, None) == _lib.WOQ_EINVAL
+    # what is gathered may not lie on itself
+    k, c = rows(), kv4()
+    for v in (rows(), rows(data=OK + 512), rows(data=OK + 1024, dtype=1)):
+        assert L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, 4, ctypes.byref(k), ctypes.byref(v),
+                            None) == _lib.WOQ_EINVAL
+
+
+def test_attention_refusals():
+    L = _lib.lib()
+
+    def call(q=None, c=None, lens=OK, batch=2, table=OK, width=1, scale=0.1, o=None, ws=1 << 21, n=1 << 30):
+        q, c, o = q or rows(heads=4, row=512), c or kv4(), o or rows(data=FAR, heads=4, row=512)
+        return L.kv4_attn(ctypes.byref(q), ctypes.byref(c), lens, batch, table, width, scale, ctypes.byref(o), ws, n, None)
+
+    for c, want in BAD_CACHES[:9]:
+        assert call(c=c) == want
+    for r, want in BAD_ROWS:
+        r = _lib.WoqRows(r.data, r.dtype, 4, r.row_stride * 2, r.head_stride)
+        if r.row_stride != 516 and r.row_stride != 520:
+            assert call(q=r) == want and call(o=r) in (want, _lib.WOQ_EINVAL)
+    assert call(q=rows(heads=3)) == call(q=rows(heads=0)) == call(q=rows(heads=2 * 65)) == _lib.WOQ_EINVAL
+    assert call(o=rows(data=FAR, heads=2)) == _lib.WOQ_EINVAL
+    assert call(o=rows(data=FAR, heads=4, row=512, dtype=1)) == _lib.WOQ_EINVAL
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        assert call(scale=scale) == _lib.WOQ_EINVAL
+    assert call(lens=None) == call(table=None) == call(batch=0) == call(batch=4097) == _lib.WOQ_EINVAL
+    assert call(lens=OK + 2) == _lib.WOQ_EALIGN and call(width=0) == _lib.WOQ_ESHAPE
+    assert call(ws=None) == call(n=64) == _lib.WOQ_EWORKSPACE and call(ws=(1 << 21) + 128) == _lib.WOQ_EALIGN
+    # o on q, or one row of it
+    assert call(o=rows(heads=4, row=512)) == _lib.WOQ_EINVAL
+    assert call(o=rows(data=OK + 4 * 512, heads=4, row=512)) == _lib.WOQ_EINVAL
+    # beside it in one array is another matter: refused only for want of a device
+    side = call(q=rows(heads=4, row=1024), o=rows(data=OK + 4 * 512, heads=4, row=1024))
+    assert side in (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE) or torch.cuda.is_available()
+
+
+def test_workspace_sizes():
+    L = _lib.lib()
+    size = L.kv4_attn_workspace_bytes
+    assert size(ctypes.byref(kv4()), 4, 1) > 0 and size(ctypes.byref(kv4()), 4, 1) % 16 == 0
+    assert size(ctypes.byref(kv4()), 4, 4096) > size(ctypes.byref(kv4()), 4, 1)
+    for c, h, b in ((kv4(dim=32), 4, 1), (kv4(), 3, 1), (kv4(), 4, 0), (kv4(), 4, 4097), (kv4(), 2 * 65, 1)):
+        assert size(ctypes.byref(c), h, b) == 0
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    with pytest.raises(ValueError):
+        woq.KV4Cache(torch.zeros(1, 1, 2, 16, 64), torch.zeros(1, 1, 16, 2, 4, dtype=torch.float16))
+    with pytest.raises(ValueError):
+        woq.KV4Cache(torch.zeros(1, 1, 2, 16, 64, dtype=torch.uint8), torch.zeros(1, 1, 16, 2, 2, dtype=torch.float16))
+    cache = woq.KV4Cache.empty(1, 1, 128, 16, device="cpu")
+    assert (cache.kv_heads, cache.dim, cache.page) == (1, 128, 16) and cache.nbytes == 16 * 144
+    x, i = torch.zeros(1, 1, 128), torch.zeros(2, dtype=torch.int32)
+    for call in (lambda: woq.kv4_append(cache, x, x, i, i[None]), lambda: woq.kv4_attn(x, cache, i[:1], i[None, :1]),
+                 lambda: woq.kv4_gather(cache, i, i[None], k_out=x, v_out=x), lambda: woq.kv4_gather(cache, i, i[None])):
+        with pytest.raises(ValueError):
+            call()
+    for name in ("kv4_append", "kv4_gather", "kv4_attn", "KV4Cache"):
+        assert name in woq.__all__

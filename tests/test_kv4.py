@@ -1,0 +1,305 @@
+"""The 4-bit cache: kv4_append and kv4_gather against the oracle's quantiser, bit for bit, and kv4_attn against
+attention in 64 bits over the values that the cache holds."""
+
+import numpy as np
+import pytest
+import torch
+
+import weight_only_bit_qgemv_b200 as woq
+from weight_only_bit_qgemv_b200 import _lib
+from tests import attn_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def packed(rng, tokens, heads, dim, dtype, spare=0):
+    """Rows of a fused array [tokens + spare, q | k | v]: k and v are slices with a stride of their own."""
+    x = torch.from_numpy(rng.standard_normal((tokens + spare, 3 * heads, dim)).astype(np.float32))
+    x = x.to(dtype).cuda()
+    return x[:, heads:2 * heads], x[:, 2 * heads:]
+
+
+def expected(k, v, cu, start, table, pages, heads, dim, page):
+    codes = np.zeros((pages, heads, 2, page, dim // 2), np.uint8)
+    scales = np.zeros((pages, heads, page, 2, dim // 32), np.float16)
+    values = {}
+    for b in range(len(cu) - 1):
+        for t in range(cu[b], cu[b + 1]):
+            at = start[b] + t - cu[b]
+            if start[b] < 0 or at // page >= table.shape[1] or not 0 <= table[b, at // page] < pages:
+                continue
+            for i, x in enumerate((k, v)):
+                q, s, val = ref.quantised(x[t].float().cpu().numpy())
+                ref.write_pages(q, s, i, codes, scales, table[b, at // page], at % page)
+                values[t, i] = val
+    return codes, scales, values
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,dim,page,lens,start", [
+    (1, 64, 16, [1], [0]),
+    (3, 128, 16, [5, 0, 33, 1], [0, 7, 15, 31]),       # odd heads; a sequence without rows; pages that end inside
+    (8, 128, 64, [64, 65, 63], [0, 0, 1]),
+    (5, 64, 32, [100, 1], [28, 200]),
+])
+def test_append_is_the_quantiser_bit_for_bit_and_gather_reads_it(dtype, heads, dim, page, lens, start):
+    rng = np.random.default_rng(heads * 100 + dim)
+    cu = np.concatenate([[2], 2 + np.cumsum(lens)]).astype(int)  # rows 0, 1 belong to no sequence
+    tokens = int(cu[-1])
+    width = max(-(-(n + s) // page) for n, s in zip(lens, start)) + 1
+    pages = len(lens) * width + 3
+    table = rng.permutation(pages)[: len(lens) * width].reshape(len(lens), width)
+    k, v = packed(rng, tokens, heads, dim, dtype, spare=3)
+    cache = woq.KV4Cache.empty(pages, heads, dim, page)
+    woq.kv4_append(cache, k, v, ints(cu), ints(table), start=ints(start))
+    codes, scales, values = expected(k, v, cu, start, table, pages, heads, dim, page)
+    assert np.array_equal(cache.codes.cpu().numpy(), codes)
+    assert np.array_equal(cache.scales.cpu().numpy().view(np.uint16), scales.view(np.uint16))
+    k2, v2 = (torch.full((tokens + 3, heads, dim), 7.0, device="cuda") for _ in "kv")
+    woq.kv4_gather(cache, ints(cu), ints(table), start=ints(start), k_out=k2, v_out=v2)
+    for i, out in enumerate((k2, v2)):
+        out = out.cpu().numpy()
+        for t in range(tokens + 3):
+            want = values[t, i] if (t, i) in values else 7.0  # rows outside the sequences stay as they were
+            assert np.array_equal(out[t], np.broadcast_to(want, out[t].shape)), (t, i)
+    k3, _ = woq.kv4_gather(cache, ints(cu), ints(table), start=ints(start), tokens=tokens, dtype=dtype)
+    assert torch.equal(k3[2:], k2[2:tokens].to(dtype)) and not k3[:2].any()
+
+
+def test_append_rounds_ties_and_extremes_as_the_quantiser():
+    """Values on and next to the codes' borders, tiny and huge blocks, zeros."""
+    heads, dim, page = 2, 128, 16
+    rng = np.random.default_rng(5)
+    x = rng.standard_normal((300, heads, dim)).astype(np.float32)
+    s = np.float32(np.float16(0.37))
+    ties = ((rng.integers(-7, 7, size=(100, heads, dim)) + 0.5) * s).astype(np.float32)
+    x[:100] = np.nextafter(ties, rng.choice([-np.inf, 0, np.inf], size=ties.shape).astype(np.float32))
+    x[:50] = ties[:50]
+    x[:100, :, ::32] = 7 * s
+    x[100:150] *= 1e-9
+    x[150:170] *= 1e-40
+    x[170:190] *= 1e5
+    x[190:200] = 0
+    x[200] = 65519.0 * 7 / 1.0001
+    k = torch.from_numpy(x).cuda()
+    cache = woq.KV4Cache.empty(20, heads, dim, page)
+    table = np.arange(20)[None]
+    woq.kv4_append(cache, k, -k, ints([0, 300]), ints(table))
+    codes, scales, _ = expected(k, -k, [0, 300], [0], table, 20, heads, dim, page)
+    assert np.array_equal(cache.codes.cpu().numpy(), codes)
+    assert np.array_equal(cache.scales.cpu().numpy().view(np.uint16), scales.view(np.uint16))
+
+
+def test_append_marks_blocks_it_cannot_hold():
+    k = torch.randn(16, 1, 64, device="cuda")
+    v = torch.randn(16, 1, 64, device="cuda")
+    k[3, 0, 5], k[4, 0, 40], v[5, 0, 0], v[6, 0, 63] = float("nan"), float("inf"), 65520.0 * 7, -float("inf")
+    cache = woq.KV4Cache.empty(1, 1, 64, 16)
+    cu, table = ints([0, 16]), ints([[0]])
+    woq.kv4_append(cache, k, v, cu, table)
+    ko, vo = woq.kv4_gather(cache, cu, table, tokens=16)
+    for out, bad in ((ko, {(3, 0), (4, 1)}), (vo, {(5, 0), (6, 1)})):
+        nan = out.isnan().view(16, 2, 32)
+        for t in range(16):
+            for b in range(2):
+                assert nan[t, b].all() if (t, b) in bad else not nan[t, b].any()
+
+
+def test_append_drops_what_has_no_page_and_touches_nothing_else():
+    cache = woq.KV4Cache.empty(4, 2, 128, 16)
+    cache.codes.fill_(0x5A)
+    cache.scales.fill_(3.0)
+    before = cache.codes.clone(), cache.scales.clone()
+    k = torch.randn(64, 2, 128, device="cuda")
+    table = ints([[-1, 4], [7, -2], [2**31 - 1, -2**31]])
+    woq.kv4_append(cache, k, k, ints([0, 20, 40, 64]), table)           # no entry names a page of the pool
+    woq.kv4_append(cache, k, k, ints([0, 64]), ints([[0]]), start=ints([16]))   # beyond the table
+    woq.kv4_append(cache, k, k, ints([0, 64]), ints([[0]]), start=ints([-3]))
+    assert torch.equal(cache.codes, before[0]) and torch.equal(cache.scales, before[1])
+    ko, vo = (torch.full((64, 2, 128), 7.0, device="cuda") for _ in "kv")
+    woq.kv4_gather(cache, ints([0, 20, 40, 64]), table, k_out=ko, v_out=vo)
+    assert not ko.any() and not vo.any()
+
+
+def random_cache(rng, pages, heads, dim, page):
+    """Every code, -8 among them, and scales of all sizes."""
+    codes = torch.from_numpy(rng.integers(0, 256, (pages, heads, 2, page, dim // 2), dtype=np.uint8)).cuda()
+    scales = torch.from_numpy((rng.standard_normal((pages, heads, page, 2, dim // 32)) * 0.2).astype(np.float16)).cuda()
+    return woq.KV4Cache(codes, scales)
+
+
+def check_attention(cache, q, lens, table, scale=None, **kw):
+    out = woq.kv4_attn(q, cache, ints(lens), ints(table), scale=scale, **kw)
+    k, v = ref.read_pages(cache.codes, cache.scales)
+    scale = cache.dim**-0.5 if scale is None else scale
+    for b, n in enumerate(lens):
+        at = [(table[b][j // cache.page], j % cache.page) for j in range(max(0, min(n, len(table[b]) * cache.page)))]
+        at = [(p, s) for p, s in at if 0 <= p < k.shape[0]]
+        kb = np.array([k[p, :, s] for p, s in at]).reshape(-1, cache.kv_heads, cache.dim)
+        vb = np.array([v[p, :, s] for p, s in at]).reshape(-1, cache.kv_heads, cache.dim)
+        want, size = ref.attend(q[b].double().cpu().numpy(), kb, vb, scale)
+        err = np.abs(out[b].double().cpu().numpy() - want)
+        assert (err <= ref.tolerance(want, size, q.dtype)).all(), (b, n, err.max())
+    assert woq.device_status() == _lib.WOQ_OK
+    return out
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("heads,kv,dim,page,lens", [
+    (1, 1, 64, 16, [1]),
+    (2, 1, 128, 16, [0, 1, 15, 16, 17, 31, 32, 33]),     # around a page, half a unit and a unit
+    (16, 8, 128, 64, [1000, 0, 129, 3]),
+    (15, 3, 128, 32, [500, 64]),                           # five query heads to a key head
+    (9, 1, 64, 64, [300, 7]),                              # nine: two passes, one of a single head
+    (64, 1, 128, 16, [257]),
+    (12, 12, 64, 128, [4096 + 5, 1]),
+])
+def test_attention_matches_the_formula(dtype, heads, kv, dim, page, lens):
+    rng = np.random.default_rng(heads * 7 + dim + page)
+    width = max(1, max(-(-n // page) for n in lens))
+    table = rng.permutation(len(lens) * width + 2)[: len(lens) * width].reshape(len(lens), width)
+    cache = random_cache(rng, len(lens) * width + 2, kv, dim, page)
+    q = torch.from_numpy(rng.standard_normal((len(lens), heads, dim)).astype(np.float32)).to(dtype).cuda()
+    check_attention(cache, q, lens, table.tolist())
+
+
+def test_attention_over_long_and_ragged_contexts():
+    """Parts that hold several sequences, and sequences that many parts share."""
+    rng = np.random.default_rng(3)
+    lens = [70001, 1, 0, 33, 4097, 12345, 2, 600] + [17] * 40
+    page, kv, dim = 64, 2, 128
+    need = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(need))
+    table = np.full((len(lens), max(need)), -1)
+    for b, n in enumerate(need):
+        table[b, :n] = order[sum(need[:b]):sum(need[:b + 1])]
+    cache = random_cache(rng, sum(need), kv, dim, page)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 4, dim)).astype(np.float32)).cuda()
+    ws = woq.kv4_attn_workspace(cache, q)
+    first = check_attention(cache, q, lens, table.tolist(), workspace=ws)
+    for _ in range(3):  # the same bits, and the workspace left ready
+        assert torch.equal(woq.kv4_attn(q, cache, ints(lens), ints(table), workspace=ws), first)
+
+
+def test_attention_keeps_precision_at_extreme_sizes():
+    """Tiny and huge queries and values; one token's scale far above the others', early and late."""
+    rng = np.random.default_rng(9)
+    page, kv, dim = 16, 1, 128
+    table = [list(range(20))]
+    for qs, ss in ((1e-20, 1.0), (1e-3, 2.0**-18), (30.0, 1.0), (1e4, 2.0**-14)):
+        cache = random_cache(rng, 20, kv, dim, page)
+        cache.scales[:, :, :, 1] *= ss
+        cache.scales[:, :, :, 0] *= min(1.0, 1.0 / qs)
+        q = torch.from_numpy((rng.standard_normal((1, 8, dim)) * qs).astype(np.float32)).cuda()
+        check_attention(cache, q, [311], table)
+    for at in (0, 150, 310):
+        cache = random_cache(rng, 20, kv, dim, page)
+        cache.scales[at // page, 0, at % page, 1] = 60000.0
+        q = torch.from_numpy(rng.standard_normal((1, 8, dim)).astype(np.float32)).cuda()
+        check_attention(cache, q, [311], table)
+    # scores far apart: all weight on a few tokens
+    cache = random_cache(rng, 20, kv, dim, page)
+    q = torch.from_numpy((40 * rng.standard_normal((1, 8, dim))).astype(np.float32)).cuda()
+    check_attention(cache, q, [320], table)
+
+
+def test_attention_ignores_what_is_not_there():
+    """NaN and infinities behind the last token, in pages of other sequences, entries outside the pool."""
+    rng = np.random.default_rng(11)
+    page, kv, dim = 32, 2, 128
+    cache = random_cache(rng, 12, kv, dim, page)
+    lens, table = [70, 5, 40], [[0, 1, 2], [3, -1, 99], [5, 12, 4]]   # of the third, tokens 32..39 have no page
+    cache.scales[2, :, 6:] = float("nan")
+    cache.scales[3, :, 5:] = float("inf")
+    cache.scales[6:] = float("nan")
+    q = torch.from_numpy(rng.standard_normal((3, 4, dim)).astype(np.float32)).cuda()
+    check_attention(cache, q, lens, table)
+    out = woq.kv4_attn(q, cache, ints([-5, 64, 2**31 - 1]), ints([[0, 1, 2], [12, -1, 0], [12, -1, -7]]))
+    assert not out.any()  # no length; no page at all
+    cache = random_cache(rng, 12, kv, dim, page)
+    check_attention(cache, q, [2**31 - 1, 96, 97], [[0, 1, 2], [3, 4, 5], [6, 7, 8]])  # longer than the table
+
+
+def test_attention_passes_on_what_is_not_finite():
+    rng = np.random.default_rng(12)
+    cache = random_cache(rng, 4, 2, 64, 16)
+    q = torch.from_numpy(rng.standard_normal((1, 4, 64)).astype(np.float32)).cuda()
+    table, lens = ints([[0, 1, 2, 3]]), ints([50])
+    clean = woq.kv4_attn(q, cache, lens, table)
+    cache.scales[1, 0, 3, 0, 1] = float("nan")  # a key of head 0
+    out = woq.kv4_attn(q, cache, lens, table)
+    assert out[0, :2].isnan().all() and torch.equal(out[0, 2:], clean[0, 2:])
+    cache = random_cache(np.random.default_rng(12), 4, 2, 64, 16)
+    cache.scales[2, 1, 0, 1, 0] = float("nan")  # block 0 of a value of head 1
+    out = woq.kv4_attn(q, cache, lens, table)
+    assert out[0, 2:, :32].isnan().all() and not out[0, 2:, 32:].isnan().any() and not out[0, :2].isnan().any()
+    q[0, 1, 7] = float("nan")
+    out = woq.kv4_attn(q, cache, lens, table)
+    assert out[0, 1].isnan().all() and not out[0, 0].isnan().any()
+
+
+def test_attention_takes_strides_and_leaves_the_rest():
+    rng = np.random.default_rng(13)
+    cache = random_cache(rng, 8, 2, 128, 16)
+    fused = torch.from_numpy(rng.standard_normal((3, 10, 128)).astype(np.float32)).cuda()
+    out = torch.full((3, 9, 128), 7.0, device="cuda")
+    lens, table = [40, 16, 1], [[0, 1, 2], [3, 4, 5], [6, 7, 0]]
+    check_attention(cache, fused[:, 2:8], lens, table, out=out[:, 1:7])
+    assert (out[:, :1] == 7).all() and (out[:, 7:] == 7).all()
+    # an output beside the queries in one array
+    both = torch.zeros(3, 12, 128, device="cuda")
+    both[:, :6] = fused[:, 2:8]
+    woq.kv4_attn(both[:, :6], cache, ints(lens), ints(table), out=both[:, 6:])
+    assert torch.equal(both[:, 6:], out[:, 1:7])
+
+
+def test_attention_on_another_stream_and_captured():
+    rng = np.random.default_rng(14)
+    cache = random_cache(rng, 64, 2, 128, 16)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 128)).astype(np.float32)).cuda()
+    lens, table = ints([500, 100]), ints(np.arange(64).reshape(2, 32))
+    want = woq.kv4_attn(q, cache, lens, table)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = woq.kv4_attn(q, cache, lens, table, stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    # one captured step, append and attention, follows the lengths that are on the device
+    ws, out = woq.kv4_attn_workspace(cache, q), torch.empty_like(q)
+    k, v = (torch.randn(2, 2, 128, device="cuda") for _ in "kv")
+    start = lens - 1
+    cu = ints([0, 1, 2])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        woq.kv4_append(cache, k, v, cu, table, start=start)
+        woq.kv4_attn(q, cache, lens, table, out=out, workspace=ws)
+    for n in ((500, 100), (17, 512), (1, 33)):
+        lens.copy_(ints(n))
+        start.copy_(lens - 1)
+        k.normal_()
+        graph.replay()
+        got = out.clone()
+        k2, _ = woq.kv4_gather(cache, cu, table, start=start, tokens=2)
+        assert (k2 - k).abs().max() <= k.abs().max() / 7 * 0.501
+        check = check_attention(cache, q, list(n), table.tolist())
+        assert torch.equal(got, check)
+
+
+def test_two_workspaces_on_two_streams():
+    rng = np.random.default_rng(15)
+    cache = random_cache(rng, 256, 2, 128, 64)
+    q = torch.from_numpy(rng.standard_normal((4, 4, 128)).astype(np.float32)).cuda()
+    lens, table = ints([4096, 4000, 3000, 17]), ints(np.arange(256).reshape(4, 64))
+    want = woq.kv4_attn(q, cache, lens, table)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [woq.kv4_attn_workspace(cache, q) for _ in streams]
+    torch.cuda.synchronize()
+    outs = [[woq.kv4_attn(q, cache, lens, table, workspace=w, stream=s) for _ in range(10)]
+            for s, w in zip(streams, spaces)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for row in outs for o in row)

@@ -46,6 +46,11 @@ __all__ = [
     "qgemm",
     "qgemm_workspace_bytes",
     "qgemm_bf16_noalloc",
+    "KV4Cache",
+    "kv4_append",
+    "kv4_gather",
+    "kv4_attn",
+    "kv4_attn_workspace",
     "device_status",
     "launch_count",
     "WoqError",
@@ -281,6 +286,166 @@ def qgemm_bf16_noalloc(X: torch.Tensor, w: PackedWeight, out: torch.Tensor | Non
     d = w.desc()
     _lib.check(_lib.lib().qgemm_bf16_noalloc(_ptr(X), m, ctypes.byref(d), _ptr(out), _stream(stream)),
                "qgemm_bf16_noalloc")
+    return out
+
+
+# ---- attention -------------------------------------------------------------------------------
+
+_DTYPES = {torch.float32: _lib.WOQ_F32, torch.float16: _lib.WOQ_F16, torch.bfloat16: _lib.WOQ_BF16}
+
+
+def _rows(t: torch.Tensor, what: str, device: int) -> _lib.WoqRows:
+    """The [rows, heads, dim] tensor ``t`` as the C ABI takes it; dim contiguous."""
+    if t.dtype not in _DTYPES or t.dim() != 3 or t.stride(2) != 1 or t.get_device() != device:
+        raise ValueError(
+            f"{what} must be a float32, float16 or bfloat16 tensor [rows, heads, dim] on the current CUDA device, "
+            "contiguous along dim"
+        )
+    row, head, _ = t.stride()
+    n, heads, dim = t.shape
+    # the stride of a dimension of one element says nothing
+    head = head if heads > 1 else dim
+    return _lib.WoqRows(t.data_ptr(), _DTYPES[t.dtype], heads, row if n > 1 else heads * head, head)
+
+
+def _ints(t: torch.Tensor, what: str, dims: int, device: int) -> int:
+    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.get_device() != device:
+        raise ValueError(f"{what} must be a contiguous {dims}-D int32 tensor on the current CUDA device")
+    return t.data_ptr()
+
+
+def _device() -> int:
+    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+
+
+@dataclass(frozen=True)
+class KV4Cache:
+    """A paged cache of keys and values in int4 blocks of 32 (layout in include/woq.h).
+
+    codes   uint8 [pages, kv_heads, 2, page, dim / 2]
+    scales  float16 [pages, kv_heads, page, 2, dim / 32]
+    """
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    def __post_init__(self):
+        c, s = self.codes, self.scales
+        if c.dtype != torch.uint8 or c.dim() != 5 or c.shape[2] != 2 or not c.is_contiguous():
+            raise ValueError("codes must be a contiguous uint8 tensor [pages, kv_heads, 2, page, dim / 2]")
+        pages, heads, _, page, half = c.shape
+        if s.dtype != torch.float16 or s.shape != (pages, heads, page, 2, half // 16) or not s.is_contiguous():
+            raise ValueError("scales must be a contiguous float16 tensor [pages, kv_heads, page, 2, dim / 32]")
+        if c.device != s.device:
+            raise ValueError("codes and scales must be on one device")
+        object.__setattr__(self, "_desc", _lib.WoqKv4(_ptr(c), _ptr(s), pages, heads, 2 * half, page))
+
+    @classmethod
+    def empty(cls, pages: int, kv_heads: int, dim: int, page: int = 64, device="cuda") -> "KV4Cache":
+        """A cache of ``pages`` pages of ``page`` tokens, zeroed."""
+        return cls(
+            torch.zeros(pages, kv_heads, 2, page, dim // 2, dtype=torch.uint8, device=device),
+            torch.zeros(pages, kv_heads, page, 2, dim // 32, dtype=torch.float16, device=device),
+        )
+
+    @property
+    def kv_heads(self) -> int:
+        return self._desc.kv_heads
+
+    @property
+    def dim(self) -> int:
+        return self._desc.dim
+
+    @property
+    def page(self) -> int:
+        return self._desc.page
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 2 * self.scales.numel()
+
+    def _on(self, device: int):
+        if self.codes.get_device() != device:
+            raise ValueError("the cache must be on the current CUDA device")
+        return ctypes.byref(self._desc)
+
+
+def _step_args(cache, k, v, cu, table, start, what):
+    d = _device()
+    c = cache._on(d)
+    kr, vr = _rows(k, f"{what}: k", d), _rows(v, f"{what}: v", d)
+    if k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.dim):
+        raise ValueError(f"{what}: k and v must be [tokens, {cache.kv_heads}, {cache.dim}]")
+    tp = _ints(table, "table", 2, d)
+    cp = _ints(cu, "cu", 1, d)
+    batch, width = table.shape
+    sp = None if start is None else _ints(start, "start", 1, d)
+    if cu.numel() != batch + 1 or (start is not None and start.numel() != batch):
+        raise ValueError(f"{what}: cu has batch + 1 entries, start and table batch")
+    return c, kr, vr, cp, sp, batch, tp, width
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, table: torch.Tensor,
+               start: torch.Tensor | None = None, stream=None) -> None:
+    """Quantise packed rows of keys and values [tokens, kv_heads, dim] into the cache's pages
+    (C ABI ``kv4_append``). Rows cu[b] .. cu[b + 1] - 1 become tokens start[b], start[b] + 1, ... of
+    sequence b, whose pages are table[b]; ``start`` None: each sequence is new."""
+    c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k, v, cu, table, start, "kv4_append")
+    rc = _lib.lib().kv4_append(c, ctypes.byref(kr), ctypes.byref(vr), k.shape[0], cp, sp, batch, tp, width,
+                               _stream(stream))
+    _lib.check(rc, "kv4_append")
+
+
+def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: torch.Tensor | None = None,
+               k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, tokens: int | None = None,
+               dtype=torch.float32, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """Read rows of the cache back (C ABI ``kv4_gather``), addressed as in kv4_append. Give ``k_out`` and
+    ``v_out`` [tokens, kv_heads, dim], or ``tokens`` (cu's last entry, which is on the device) for new
+    ones of ``dtype``, zero where no sequence has the row."""
+    if (k_out is None) != (v_out is None) or (k_out is None and tokens is None):
+        raise ValueError("kv4_gather takes k_out and v_out, or tokens")
+    if k_out is None:
+        shape = (tokens, cache.kv_heads, cache.dim)
+        k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.codes.device) for _ in "kv")
+    c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k_out, v_out, cu, table, start, "kv4_gather")
+    rc = _lib.lib().kv4_gather(c, cp, sp, batch, tp, width, k_out.shape[0], ctypes.byref(kr), ctypes.byref(vr),
+                               _stream(stream))
+    _lib.check(rc, "kv4_gather")
+    return k_out, v_out
+
+
+def kv4_attn_workspace(cache: KV4Cache, q: torch.Tensor) -> torch.Tensor:
+    """A zeroed workspace for kv4_attn calls with queries shaped like ``q`` (every call leaves its
+    counters zero; calls that share one must be ordered on one stream)."""
+    need = _lib.lib().kv4_attn_workspace_bytes(ctypes.byref(cache._desc), q.shape[1], q.shape[0])
+    return torch.zeros(int(need), dtype=torch.uint8, device=cache.codes.device)
+
+
+def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.Tensor, scale: float | None = None,
+             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One-token attention [batch, heads, dim] over the first lens[b] cached tokens of each sequence
+    (C ABI ``kv4_attn``). ``scale`` defaults to dim^-1/2; without ``workspace`` one is made for the
+    call."""
+    d = _device()
+    c = cache._on(d)
+    qr = _rows(q, "q", d)
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    orow = _rows(out, "out", d)
+    lp, tp = _ints(lens, "lens", 1, d), _ints(table, "table", 2, d)
+    batch, width = table.shape
+    if q.shape[0] != batch or lens.shape[0] != batch or q.shape[2] != cache.dim or out.shape != q.shape:
+        raise ValueError("q and out must be [batch, heads, dim] of the cache's dim, lens [batch], table [batch, width]")
+    if workspace is None:
+        # made, zeroed and given back on the stream that uses it
+        with torch.cuda.stream(stream):
+            workspace = kv4_attn_workspace(cache, q)
+    elif workspace.get_device() != d or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    rc = _lib.lib().kv4_attn(ctypes.byref(qr), c, lp, batch, tp, width, cache.dim**-0.5 if scale is None else scale,
+                             ctypes.byref(orow), _ptr(workspace), workspace.numel() * workspace.element_size(),
+                             _stream(stream))
+    _lib.check(rc, "kv4_attn")
     return out
 
 

@@ -31,6 +31,9 @@ WOQ_EPI_NONE = 0
 WOQ_EPI_SWIGLU = 1
 WOQ_EPI_RESIDUAL = 2
 WOQ_CHAIN_MAX_ITEMS = 8
+WOQ_F32 = 0
+WOQ_F16 = 1
+WOQ_BF16 = 2
 
 #: Every symbol include/woq.h declares.
 EXPORTS = (
@@ -45,6 +48,10 @@ EXPORTS = (
     "qgemm_workspace_bytes",
     "qgemm",
     "qgemm_bf16_noalloc",
+    "kv4_append",
+    "kv4_gather",
+    "kv4_attn_workspace_bytes",
+    "kv4_attn",
     "woq_device_status",
     "woq_debug_set_wait_limit",
     "woq_status_str",
@@ -71,6 +78,27 @@ class WoqChainItem(ctypes.Structure):
         ("y", ctypes.c_void_p),
         ("r", ctypes.c_void_p),
         ("epilogue", ctypes.c_int32),
+    ]
+
+
+class WoqRows(ctypes.Structure):
+    _fields_ = [
+        ("data", ctypes.c_void_p),
+        ("dtype", ctypes.c_int32),
+        ("heads", ctypes.c_int32),
+        ("row_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+    ]
+
+
+class WoqKv4(ctypes.Structure):
+    _fields_ = [
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("pages", ctypes.c_int64),
+        ("kv_heads", ctypes.c_int32),
+        ("dim", ctypes.c_int32),
+        ("page", ctypes.c_int32),
     ]
 
 
@@ -118,6 +146,15 @@ def lib() -> ctypes.CDLL:
     L.qgemm.restype = ctypes.c_int
     L.qgemm_bf16_noalloc.argtypes = [vp, c_i64, wp, vp, vp]
     L.qgemm_bf16_noalloc.restype = ctypes.c_int
+    rp, cp = ctypes.POINTER(WoqRows), ctypes.POINTER(WoqKv4)
+    L.kv4_append.argtypes = [cp, rp, rp, c_i64, vp, vp, c_i32, vp, c_i64, vp]
+    L.kv4_append.restype = ctypes.c_int
+    L.kv4_gather.argtypes = [cp, vp, vp, c_i32, vp, c_i64, c_i64, rp, rp, vp]
+    L.kv4_gather.restype = ctypes.c_int
+    L.kv4_attn_workspace_bytes.argtypes = [cp, c_i32, c_i32]
+    L.kv4_attn_workspace_bytes.restype = ctypes.c_size_t
+    L.kv4_attn.argtypes = [rp, cp, vp, c_i32, vp, c_i64, ctypes.c_float, rp, vp, ctypes.c_size_t, vp]
+    L.kv4_attn.restype = ctypes.c_int
     L.woq_device_status.argtypes = [ctypes.c_int]
     L.woq_device_status.restype = ctypes.c_int
     L.woq_debug_set_wait_limit.argtypes = [ctypes.c_longlong]

@@ -1,0 +1,147 @@
+// C-ABI entry points of the attention calls (declared in include/woq.h): argument checks, the
+// device check and dispatch to the kernel launchers. Nothing here allocates or synchronises.
+#include <cmath>
+#include <cstdint>
+
+#include "woq.h"
+#include "woq_internal.h"
+
+namespace woq {
+namespace {
+
+constexpr int kMaxHeads = 1 << 16;
+constexpr int kMaxGroup = 64;
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+int64_t size_of(int32_t dtype) { return dtype == WOQ_F32 ? 4 : 2; }
+
+int check_rows(const woq_rows *r, int64_t heads, int64_t dim) {
+  if (!r || !r->data) return WOQ_EINVAL;
+  if (r->dtype != WOQ_F32 && r->dtype != WOQ_F16 && r->dtype != WOQ_BF16) return WOQ_EINVAL;
+  if (r->heads != heads) return WOQ_EINVAL;
+  const int64_t unit = 16 / size_of(r->dtype);
+  // strides below 2^40 elements: offsets stay far from the end of 64 bits for any count of rows
+  if (r->row_stride <= 0 || r->head_stride < dim || r->row_stride >= (int64_t(1) << 40) ||
+      r->head_stride >= (int64_t(1) << 40) || r->row_stride % unit || r->head_stride % unit)
+    return WOQ_ESHAPE;
+  return aligned(r->data, 16) ? WOQ_OK : WOQ_EALIGN;
+}
+
+int check_cache(const woq_kv4 *c) {
+  if (!c || !c->codes || !c->scales) return WOQ_EINVAL;
+  if (c->page < 16 || c->page > 65536 || (c->page & (c->page - 1))) return WOQ_EINVAL;
+  if (c->dim != 64 && c->dim != 128) return WOQ_ESHAPE;
+  if (c->kv_heads < 1 || c->kv_heads > 1024 || c->pages < 1 || c->pages > INT32_MAX) return WOQ_ESHAPE;
+  return aligned(c->codes, 64) && aligned(c->scales, 64) ? WOQ_OK : WOQ_EALIGN;
+}
+
+int check_table(int32_t batch, const int32_t *table, int64_t width) {
+  if (!table || batch < 1 || batch > kKv4MaxBatch) return WOQ_EINVAL;
+  if (width < 1 || width > INT32_MAX) return WOQ_ESHAPE;
+  return aligned(table, 4) ? WOQ_OK : WOQ_EALIGN;
+}
+
+// First and one past the last byte of [rows, heads, dim].
+struct Span {
+  uintptr_t first, last;
+};
+Span span(const woq_rows &r, int64_t rows, int64_t dim) {
+  const uintptr_t p = reinterpret_cast<uintptr_t>(r.data);
+  const int64_t last = (rows - 1) * r.row_stride + (r.heads - 1) * r.head_stride + dim;
+  return {p, p + static_cast<uintptr_t>(last * size_of(r.dtype))};
+}
+
+// Whether an output shares bytes with an input. Slices of one fused array interleave without
+// sharing: with equal strides, rows apart by less than a row are compared within one row.
+bool overlap(const woq_rows &a, const woq_rows &b, int64_t rows, int64_t dim) {
+  const Span x = span(a, rows, dim), y = span(b, rows, dim);
+  if (x.last <= y.first || y.last <= x.first) return false;
+  const int64_t size = size_of(a.dtype);
+  const uintptr_t pitch = static_cast<uintptr_t>(a.row_stride * size);
+  if (size != size_of(b.dtype) || a.row_stride != b.row_stride) return true;
+  const uintptr_t in_a = static_cast<uintptr_t>(((a.heads - 1) * a.head_stride + dim) * size);
+  const uintptr_t in_b = static_cast<uintptr_t>(((b.heads - 1) * b.head_stride + dim) * size);
+  const uintptr_t d = x.first <= y.first ? (y.first - x.first) % pitch : pitch - (x.first - y.first) % pitch;
+  // b's row starts d bytes into a row of a: apart if it begins behind a's heads and ends before the next row
+  return !(d % pitch >= in_a && d % pitch + in_b <= pitch);
+}
+
+int check_step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+               const int32_t *start, int32_t batch, const int32_t *table, int64_t width) {
+  int rc = check_cache(cache);
+  if (rc != WOQ_OK) return rc;
+  rc = check_table(batch, table, width);
+  if (rc != WOQ_OK) return rc;
+  if (!cu || tokens < 0) return WOQ_EINVAL;
+  if (tokens > INT32_MAX) return WOQ_ESHAPE;
+  if (!aligned(cu, 4) || !aligned(start, 4)) return WOQ_EALIGN;
+  rc = check_rows(k, cache->kv_heads, cache->dim);
+  return rc != WOQ_OK ? rc : check_rows(v, cache->kv_heads, cache->dim);
+}
+
+int step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+         const int32_t *start, int32_t batch, const int32_t *table, int64_t width, bool append, void *stream) {
+  int rc = check_step(cache, k, v, tokens, cu, start, batch, table, width);
+  if (rc != WOQ_OK) return rc;
+  if (!append && tokens > 0 && overlap(*k, *v, tokens, cache->dim)) return WOQ_EINVAL;
+  DevInfo dev;
+  rc = current_device(&dev);
+  if (rc != WOQ_OK || tokens == 0) return rc;
+  return launch_kv4_rows(*cache, *k, *v, tokens, cu, start, batch, table, width, append,
+                         static_cast<cudaStream_t>(stream), dev);
+}
+
+}  // namespace
+}  // namespace woq
+
+using woq::DevInfo;
+
+extern "C" {
+
+int kv4_append(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+               const int32_t *start, int32_t batch, const int32_t *table, int64_t width, void *stream) {
+  return woq::step(cache, k, v, tokens, cu, start, batch, table, width, true, stream);
+}
+
+int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, int32_t batch, const int32_t *table,
+               int64_t width, int64_t tokens, const woq_rows *k, const woq_rows *v, void *stream) {
+  return woq::step(cache, k, v, tokens, cu, start, batch, table, width, false, stream);
+}
+
+size_t kv4_attn_workspace_bytes(const woq_kv4 *cache, int32_t q_heads, int32_t batch) {
+  if (woq::check_cache(cache) != WOQ_OK || batch < 1 || batch > woq::kKv4MaxBatch) return 0;
+  if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > woq::kMaxGroup) return 0;
+  DevInfo dev;
+  const int sms = woq::current_device(&dev) == WOQ_OK ? dev.sm_count : 148;
+  return woq::kv4_attn_workspace(batch, cache->kv_heads, q_heads / cache->kv_heads, cache->dim, sms);
+}
+
+int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32_t batch, const int32_t *table,
+             int64_t width, float scale, const woq_rows *o, void *workspace, size_t workspace_bytes,
+             void *stream) {
+  int rc = woq::check_cache(cache);
+  if (rc != WOQ_OK) return rc;
+  rc = woq::check_table(batch, table, width);
+  if (rc != WOQ_OK) return rc;
+  if (!q || !o || !lens) return WOQ_EINVAL;
+  if (q->heads < 1 || q->heads % cache->kv_heads || q->heads / cache->kv_heads > woq::kMaxGroup) return WOQ_EINVAL;
+  rc = woq::check_rows(q, q->heads, cache->dim);
+  if (rc != WOQ_OK) return rc;
+  rc = woq::check_rows(o, q->heads, cache->dim);
+  if (rc != WOQ_OK) return rc;
+  if (o->dtype != q->dtype || !(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
+  if (!woq::aligned(lens, 4)) return WOQ_EALIGN;
+  if (woq::overlap(*q, *o, batch, cache->dim)) return WOQ_EINVAL;
+  DevInfo dev;
+  rc = woq::current_device(&dev);
+  const size_t need = woq::kv4_attn_workspace(batch, cache->kv_heads, q->heads / cache->kv_heads, cache->dim,
+                                              rc == WOQ_OK ? dev.sm_count : 148);
+  if (!workspace || workspace_bytes < need) return WOQ_EWORKSPACE;
+  if (!woq::aligned(workspace, 256)) return WOQ_EALIGN;
+  if (rc != WOQ_OK) return rc;
+  return woq::launch_kv4_attn(*q, *cache, lens, batch, table, width, scale, *o, workspace,
+                              static_cast<cudaStream_t>(stream), dev);
+}
+
+}  // extern "C"

@@ -1,0 +1,648 @@
+// kv4_attn: one query token a sequence against its cached keys and values, held in 4 bits.
+//   s_j = scale q . k_j,   p = softmax(s over the sequence's tokens),   o = sum_j p_j v_j
+// with k_j[d] = ks[j, d / 32] * kc[j, d] and v_j likewise (binary16 scales, int4 codes).
+//
+// Bound: memory. A token and key head is dim + dim / 8 bytes for 4 * dim * (query heads a key head)
+// flop; 144 bytes at dim 128. On the CUDA cores the unpacking and one multiply a query head would
+// already exceed what the bytes' time leaves, so both products run as warp matrix instructions
+// (mma.sync m16n8k16, binary16 in, FP32 out) on codes that never leave 4 bits as numbers: a nibble
+// under a mask IS a binary16 number, the subnormal u * 2^-24 (u = code + 8; u * 2^-20 for the
+// nibble above), which the tensor cores multiply exactly. Unpacking is one logic instruction for
+// two codes. tcgen05 would want the codes widened fourfold in shared memory first, and its 128 rows
+// would be 94 % empty at 8 query heads.
+//
+// FP32 accuracy: the 16 rows of the left operand are 8 query heads' high binary16 parts and the
+// same heads' low parts, so that 22 bits of q, and then of p_j * vs[j, block], take part. The
+// query is scaled by a power of two into binary16's range, the weights likewise (see `room`). Per block
+// of 32 the key scale multiplies an FP32 block sum. The u = code + 8 offset is taken off by the sums'
+// starting values: -8 sum(q) for a key block, -8 sum(p vs), itself a product with a constant
+// operand, for a value block. Sums inside the matrix instructions run over 32 tokens at most; from
+// there on they are FP32 additions, rounded to nearest.
+//
+// The left operand of the second product is the result of the first without leaving its registers.
+//
+// Split: all sequences' tokens, in units of 32 per (sequence, key head), are one line that is cut into
+// equal parts, one for each block, whatever the lengths are: the lengths are read on the device. A part that
+// covers only some of a (sequence, key head) leaves its sum, maximum and total in the workspace;
+// the last of the blocks concerned adds them in the order of the tokens (the same bits on every call).
+//
+// Each warp takes every fourth unit through its own ring of shared memory, filled by bulk copies
+// (three per 16 tokens: keys, values, scales are each contiguous within a page).
+#include <algorithm>
+#include <mutex>
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+#include "woq_internal.h"
+
+namespace woq {
+
+__device__ unsigned int g_kv4_timeout_flag = 0;
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kBlocksPerSm = 4;
+constexpr int kUnit = 32;      // tokens of a unit
+constexpr int kStages = 2;     // units in a warp's ring
+constexpr int kHeads = 8;      // query heads of a pass: half the rows of a matrix instruction
+constexpr int kMinUnits = 4;   // units of a part, at least: one for each warp
+constexpr long long kWaitLimit = 1LL << 32;  // cycles (~2 s)
+
+template <int D>
+struct Shape {
+  static constexpr int NB = D / 32;                   // blocks of a row
+  static constexpr int RowBytes = D / 2;
+  static constexpr int ScaleBytes = 4 * NB;           // of a token: key and value
+  static constexpr int Half = 16 * (2 * RowBytes + ScaleBytes);  // 16 tokens: keys, values, scales
+  static constexpr int Stage = 2 * Half;
+  static constexpr int Slot = kHeads * (D + 2);       // floats of a partial result
+};
+
+struct Args {
+  woq_rows q, o;
+  const uint8_t *codes;
+  const uint8_t *scales;
+  const int32_t *lens, *table;
+  int64_t pages, width;
+  int batch, shift, kv_heads, group, chunks;
+  float scale;
+  unsigned *counters;
+  float *partials;
+  long long wait_limit;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void mma(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1, const float (&c)[4]) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%12,%13};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
+}
+
+// Two codes of a word as u = code + 8 in binary16 subnormals: u * 2^-24, and u * 2^-20.
+__device__ __forceinline__ uint32_t low(uint32_t w) { return (w & 0x000f000fu) ^ 0x00080008u; }
+__device__ __forceinline__ uint32_t high(uint32_t w) { return (w & 0x00f000f0u) ^ 0x00800080u; }
+
+// a and b as binary16 high parts and binary16 remainders: 22 bits of each.
+__device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t *>(&h);
+  lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// The token of a 16-token half that column 2 t + j of its matrix i (of two, 8 tokens each) holds: a quad
+// lane's two tokens lie four apart, which spreads the value rows that a half-warp reads over all banks.
+__device__ __forceinline__ int token_of(int i, int t, int j) { return 8 * i + t + 4 * j; }
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const Args a) {
+  using S = Shape<D>;
+  constexpr int NB = S::NB;
+  extern __shared__ __align__(128) uint8_t smem[];
+  // [ring: kWarps * kStages * Stage][q operands: 2 NB * 32 * 16][bars][corr, fac][prefix]
+  uint8_t *ring = smem;
+  uint4 *qop = reinterpret_cast<uint4 *>(smem + kWarps * kStages * S::Stage);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(qop + 2 * NB * 32);
+  float *corr = reinterpret_cast<float *>(bars + kWarps * kStages);  // [kHeads][NB]
+  float *fac = corr + kHeads * NB;                                   // [kHeads]
+  int *flags = reinterpret_cast<int *>(fac + kHeads);                // abort, last
+  int64_t *pre = reinterpret_cast<int64_t *>(flags + 4);             // [batch + 1]: units before a sequence
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  volatile int *abort = flags;
+
+  if (tid == 0) {
+    for (int i = 0; i < kWarps * kStages; ++i) ptx::mbar_init(&bars[i], 1);
+    ptx::fence_mbar_init();
+    flags[0] = 0;
+    pre[0] = 0;
+  }
+  ptx::pdl_wait();
+
+  // Units of each sequence, summed up.
+  const int64_t longest = a.width << a.shift;
+  auto units_of = [&](int b) -> int64_t {
+    int64_t n = a.lens[b];
+    n = n < 0 ? 0 : n > longest ? longest : n;
+    return (n + kUnit - 1) / kUnit;
+  };
+  if (warp == 0) {
+    int64_t carry = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      int64_t n = b0 + lane < a.batch ? units_of(b0 + lane) : 0;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const int64_t m = __shfl_up_sync(0xffffffffu, n, i);
+        if (lane >= i) n += m;
+      }
+      if (b0 + lane < a.batch) pre[b0 + lane + 1] = carry + n;
+      carry += __shfl_sync(0xffffffffu, n, 31);
+    }
+  }
+  __syncthreads();
+
+  const int heads = a.kv_heads * a.chunks;  // passes of a sequence: key heads times chunks of 8 query heads
+  const int64_t total = pre[a.batch] * heads;
+  int64_t parts = (total + kMinUnits - 1) / kMinUnits;
+  if (parts > gridDim.x) parts = gridDim.x;
+
+  // Sequences without tokens: zeros.
+  for (int b = blockIdx.x; b < a.batch; b += gridDim.x) {
+    if (pre[b + 1] != pre[b]) continue;
+    const int n4 = a.kv_heads * a.group * (D / 4);
+    for (int i = tid; i < n4; i += kThreads)
+      store4(a.o.data, b * a.o.row_stride + (i / (D / 4)) * a.o.head_stride + 4 * (i % (D / 4)), a.o.dtype,
+             make_float4(0, 0, 0, 0));
+  }
+
+  const int64_t begin = blockIdx.x < parts ? blockIdx.x * total / parts : 0;
+  const int64_t end = blockIdx.x < parts ? (blockIdx.x + 1) * total / parts : 0;
+  uint32_t phases = 0;  // parity of each stage of this warp's ring
+  uint8_t *mine = ring + warp * kStages * S::Stage;
+  uint64_t *bar = bars + warp * kStages;
+
+  for (int64_t cur = begin; cur < end;) {
+    // The sequence, key head and chunk of unit `cur`.
+    int lo = 0, hi = a.batch;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (pre[mid] * heads <= cur) lo = mid;
+      else hi = mid;
+    }
+    const int b = lo;
+    const int64_t units = pre[b + 1] - pre[b];
+    const int64_t at = cur - pre[b] * heads;
+    const int pass = static_cast<int>(at / units);
+    const int64_t u_begin = at % units;
+    const int64_t u_end = u_begin + ((end - cur) < (units - u_begin) ? (end - cur) : (units - u_begin));
+    const int kvh = pass / a.chunks, h0 = (pass % a.chunks) * kHeads;
+    const int nh = a.group - h0 < kHeads ? a.group - h0 : kHeads;
+    int64_t len = a.lens[b];
+    len = len > longest ? longest : len;
+
+    // One unit's copies into stage `st`, by lane 0. e0, e1: the table's entries for its halves.
+    const int32_t *row = a.table + b * a.width;
+    auto entry = [&](int64_t u, int half) -> int32_t {
+      const int64_t key = u * kUnit + 16 * half;
+      return u < u_end && key < len ? row[key >> a.shift] : -1;
+    };
+    auto good = [&](int32_t e) { return e >= 0 && e < a.pages; };
+    auto issue = [&](int64_t u, int st, int32_t e0, int32_t e1) {
+      if (lane != 0 || u >= u_end) return;
+      const uint32_t bytes = (good(e0) ? S::Half : 0) + (good(e1) ? S::Half : 0);
+      ptx::mbar_arrive_expect_tx(&bar[st], bytes);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const int32_t e = half ? e1 : e0;
+        if (!good(e)) continue;
+        const int64_t page = int64_t(1) << a.shift;
+        const int64_t slot = (u * kUnit + 16 * half) & (page - 1);
+        const int64_t head = static_cast<int64_t>(e) * a.kv_heads + kvh;
+        uint8_t *dst = mine + st * S::Stage + half * S::Half;
+        ptx::bulk_load(dst, a.codes + (head * 2 * page + slot) * S::RowBytes, 16 * S::RowBytes, &bar[st]);
+        ptx::bulk_load(dst + 16 * S::RowBytes, a.codes + ((head * 2 + 1) * page + slot) * S::RowBytes,
+                       16 * S::RowBytes, &bar[st]);
+        ptx::bulk_load(dst + 32 * S::RowBytes, a.scales + (head * page + slot) * S::ScaleBytes,
+                       16 * S::ScaleBytes, &bar[st]);
+      }
+    };
+    const int64_t u0 = u_begin + warp;
+    int32_t e[kStages + 1][2];  // entries of the units in the ring and of the one after
+#pragma unroll
+    for (int s = 0; s <= kStages; ++s)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) e[s][h] = entry(u0 + s * kWarps, h);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) issue(u0 + s * kWarps, s, e[s][0], e[s][1]);
+
+    // The query: rows h0 .. h0 + nh - 1 of this key head, times scale * log2(e), times the power of two
+    // that brings the row's largest into [2^13, 2^14).
+    for (int r = warp; r < kHeads; r += kWarps) {
+      float v[D / 32];
+      float big = 0;
+      const int64_t base = b * a.q.row_stride + (static_cast<int64_t>(kvh) * a.group + h0 + r) * a.q.head_stride;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {  // lane = element of block i
+        float x = 0;
+        if (r < nh) {
+          const int64_t p = base + 32 * i + lane;
+          x = a.q.dtype == WOQ_F32   ? static_cast<const float *>(a.q.data)[p]
+              : a.q.dtype == WOQ_F16 ? __half2float(static_cast<const __half *>(a.q.data)[p])
+                                     : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q.data)[p]);
+        }
+        v[i] = x * a.scale;
+        big = fmaxf(big, fabsf(v[i]));
+      }
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, i));
+      int ex = 0;
+      if (big > 0 && big < INFINITY) ex = max(ilogbf(big) - 13, -100);
+      const float up = ldexpf(1.0f, -ex);
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        v[i] *= up;
+        float sum = v[i];
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
+        if (lane == 0) corr[r * NB + i] = sum * (-8.0f / 16777216.0f);
+        // Element `lane` = 8 tt + n of the block: matrix step 2 i + (n / 2 % 2), a or second pair by n % 2,
+        // first or second of the pair by n / 4; odd n meet codes 16 times too large.
+        const int n = lane & 7, tt = lane >> 3;
+        const float x = n & 1 ? v[i] * 0.0625f : v[i];
+        const __half h = __float2half_rn(x);
+        const __half l = __float2half_rn(x - __half2float(h));
+        __half *dst = reinterpret_cast<__half *>(qop + (2 * i + (n >> 1 & 1)) * 32 + (r * 4 + tt)) +
+                      4 * (n & 1) + (n >> 2);
+        dst[0] = h;  // .x / .z: high parts (rows 0..7)
+        dst[2] = l;  // .y / .w: low parts (rows 8..15)
+      }
+      if (lane == 0) fac[r] = ldexpf(1.0f, 24 + ex);
+    }
+    __syncthreads();
+
+    float kc[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) kc[i] = corr[g * NB + i];
+    const float f = fac[g];
+
+    float m = -INFINITY;  // running maximum of the scores (log2), shared by the quad
+    float l = 0;          // this lane's sum of p
+    // p = 2^(s - m + room): the power 2^room lifts p * vs to the middle of binary16's range, so that
+    // what lies below its smallest number is below 2^-28 of the largest. It cancels in o / sum(p).
+    float room = 0, limit = -1;
+    float2 acc[NB][4];  // value block, n-tile: columns of tokens' head g, dims 32 b + 8 t + i and + 4
+#pragma unroll
+    for (int i = 0; i < NB; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0, 0);
+
+    int st = 0;
+    bool ok = true;
+    for (int64_t u = u0; u < u_end; u += kWarps) {
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(&bar[st], phases >> st & 1, a.wait_limit, abort))) {
+        *abort = 1;
+        atomicOr(&g_kv4_timeout_flag, 1u);
+        ok = false;
+        break;
+      }
+      phases ^= 1u << st;
+      const uint8_t *base = mine + st * S::Stage;
+
+      // ---- scores: two matrices of 8 tokens for each half of the unit ----
+      float2 s[2][2];
+      uint32_t vs[2][2][2][NB / 2];  // value scales: half, matrix, token, pairs of blocks
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint8_t *hb = base + h * S::Half;
+        const bool page_ok = good(e[0][h]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // column g of the matrix is token 8 i + (g / 2) + 4 (g % 2)
+          const uint8_t *kr = hb + token_of(i, g >> 1, g & 1) * S::RowBytes + t * (4 * NB);
+          uint32_t w[NB];
+          if constexpr (NB == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(kr);
+            w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2 *>(kr);
+            w[0] = x.x; w[1] = x.y;
+          }
+          // scales of this lane's two tokens, 0 where there is no token
+          uint32_t ks[2][NB / 2];
+          bool live[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int tok = token_of(i, t, j);
+            live[j] = page_ok && u * kUnit + 16 * h + tok < len;
+            const uint8_t *sr = hb + 32 * S::RowBytes + tok * S::ScaleBytes;
+            if constexpr (NB == 4) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(sr);
+              ks[j][0] = x.x; ks[j][1] = x.y;
+              vs[h][i][j][0] = live[j] ? x.z : 0; vs[h][i][j][1] = live[j] ? x.w : 0;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2 *>(sr);
+              ks[j][0] = x.x;
+              vs[h][i][j][0] = live[j] ? x.y : 0;
+            }
+          }
+          float2 sum = make_float2(0, 0);
+#pragma unroll
+          for (int k = 0; k < NB; ++k) {
+            float c[4] = {kc[k], kc[k], 0, 0};
+            mma(c, qop[(2 * k) * 32 + lane], low(w[k]), high(w[k]), c);
+            const uint32_t w8 = w[k] >> 8;
+            mma(c, qop[(2 * k + 1) * 32 + lane], low(w8), high(w8), c);
+            const __half2 s0 = *reinterpret_cast<const __half2 *>(&ks[0][k / 2]);
+            const __half2 s1 = *reinterpret_cast<const __half2 *>(&ks[1][k / 2]);
+            const float2 sc = make_float2(k & 1 ? __high2float(s0) : __low2float(s0),
+                                          k & 1 ? __high2float(s1) : __low2float(s1));
+            sum = __ffma2_rn(__fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])), sc, sum);
+          }
+          sum = __fmul2_rn(sum, make_float2(f, f));
+          s[h][i] = make_float2(live[0] ? sum.x : -INFINITY, live[1] ? sum.y : -INFINITY);
+        }
+      }
+
+      // ---- largest value scale: keep p * vs inside binary16 ----
+      __half2 big = __float2half2_rn(0);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int k = 0; k < NB / 2; ++k)
+              big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&vs[h][i][j][k])));
+      const float most = fmaxf(__low2float(big), __high2float(big));
+      float shift = 0;  // change of room
+      if (__any_sync(0xffffffffu, most > limit)) {
+        float all = most;
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
+        // largest p * vs below 2^4 now, up to 2^15 (limit) before room changes again
+        const float next = all > 0 && all < INFINITY ? 3.0f - static_cast<float>(ilogbf(all)) : 0.0f;
+        shift = next - room;
+        room = next;
+        limit = ldexpf(1.0f, 15 - static_cast<int>(next));
+      }
+
+      // ---- softmax over the unit ----
+      float mx = fmaxf(fmaxf(fmaxf(s[0][0].x, s[0][0].y), fmaxf(s[0][1].x, s[0][1].y)),
+                       fmaxf(fmaxf(s[1][0].x, s[1][0].y), fmaxf(s[1][1].x, s[1][1].y)));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+      // Any token makes the maximum finite, so that -infinity means that there was none: a row of
+      // scores that are all NaN or -infinity gives NaN, as the formula does.
+      if (good(e[0][0]) || good(e[0][1])) mx = fmaxf(mx, -3.402823466e38f);
+      const float m2 = fmaxf(m, mx);
+      const float ref = (m2 == -INFINITY ? 0.0f : m2) - room;
+      const float alpha = ex2((m == -INFINITY ? -INFINITY : m - (m2 - shift)));
+      m = m2;
+      l *= alpha;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          s[h][i] = make_float2(ex2(s[h][i].x - ref), ex2(s[h][i].y - ref));
+          l += s[h][i].x + s[h][i].y;
+        }
+
+      // ---- values ----
+      const float2 al = make_float2(alpha, alpha);
+#pragma unroll
+      for (int kp = 0; kp < NB / 2; ++kp) {  // pairs of blocks: one word of a lane's codes
+        uint32_t v[2][2][2];  // half, matrix, block of the pair: two tokens' four codes
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint8_t *vr = base + h * S::Half + 16 * S::RowBytes + g * (2 * NB) + kp * 4;
+            const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 0) * S::RowBytes);
+            const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 1) * S::RowBytes);
+            v[h][i][0] = __byte_perm(w0, w1, 0x5410);
+            v[h][i][1] = __byte_perm(w0, w1, 0x7632);
+          }
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+          const int k = 2 * kp + kb;
+          uint4 p[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float2 x[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const __half2 s0 = *reinterpret_cast<const __half2 *>(&vs[h][i][0][kp]);
+              const __half2 s1 = *reinterpret_cast<const __half2 *>(&vs[h][i][1][kp]);
+              x[i] = __fmul2_rn(s[h][i], make_float2(kb ? __high2float(s0) : __low2float(s0),
+                                                     kb ? __high2float(s1) : __low2float(s1)));
+            }
+            split(x[0].x, x[0].y, p[h].x, p[h].y);
+            split(x[1].x, x[1].y, p[h].z, p[h].w);
+          }
+          // -8 sum(p vs) in the units of the codes' two places
+          float c1[4] = {0, 0, 0, 0}, c16[4] = {0, 0, 0, 0};
+          mma(c1, p[0], 0x80088008u, 0x80088008u, c1);
+          mma(c1, p[1], 0x80088008u, 0x80088008u, c1);
+          mma(c16, p[0], 0x80808080u, 0x80808080u, c16);
+          mma(c16, p[1], 0x80808080u, 0x80808080u, c16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float c[4];
+            const int sh = 8 * (i >> 1);
+            auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh) : low(w >> sh); };
+            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), i & 1 ? c16 : c1);
+            mma(c, p[1], pick(v[1][0][kb]), pick(v[1][1][kb]), c);
+            acc[k][i] = __ffma2_rn(acc[k][i], al, __fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
+          }
+        }
+      }
+
+      __syncwarp();  // every lane has read the stage
+      e[0][0] = e[1][0]; e[0][1] = e[1][1];
+#pragma unroll
+      for (int i = 1; i < kStages; ++i) { e[i][0] = e[i + 1][0]; e[i][1] = e[i + 1][1]; }
+      issue(u + kStages * kWarps, st, e[kStages - 1][0], e[kStages - 1][1]);
+      e[kStages][0] = entry(u + (kStages + 1) * kWarps, 0);
+      e[kStages][1] = entry(u + (kStages + 1) * kWarps, 1);
+      st = st + 1 == kStages ? 0 : st + 1;
+    }
+    if (!ok) {
+      // The copies that this warp still has in flight end before the block does.
+      int never = 0;
+      for (int i = 0; i < kStages; ++i) ptx::mbar_wait_bounded(&bar[i], phases >> i & 1, 1LL << 28, &never);
+    }
+
+    // ---- the four warps' results, then the block's ----
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();  // the ring is idle: it takes the warps' results
+    float *res = reinterpret_cast<float *>(ring) + warp * S::Slot;
+    // m as the reference that p was taken against
+    if (t == 0) {
+      res[kHeads * D + g] = m == -INFINITY ? -INFINITY : m - room;
+      res[kHeads * D + kHeads + g] = l;
+    }
+#pragma unroll
+    for (int k = 0; k < NB; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float unit = i & 1 ? 1048576.0f : 16777216.0f;  // 2^20, 2^24
+        res[g * D + 32 * k + 8 * t + i] = acc[k][i].x * unit;
+        res[g * D + 32 * k + 8 * t + 4 + i] = acc[k][i].y * unit;
+      }
+    __syncthreads();
+
+    // Thread: head tid / 16, D / 16 dims from (tid % 16) * 4 on, 64 apart.
+    const int hd = tid >> 4, d0 = (tid & 15) * 4;
+    constexpr int ND = D / 64;
+    // Adds one result (a warp's or a part's) to the running one, in the order of the calls.
+    float M = -INFINITY, L = 0;
+    float4 o[ND];
+    auto reset = [&] {
+      M = -INFINITY;
+      L = 0;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) o[i] = make_float4(0, 0, 0, 0);
+    };
+    auto add = [&](const float *r, auto ld, auto ld4) {
+      const float mk = ld(r + kHeads * D + hd), lk = ld(r + kHeads * D + kHeads + hd);
+      if (mk == -INFINITY) return;  // no token seen
+      const float M2 = fmaxf(M, mk);
+      const float x = M == -INFINITY ? 0.0f : ex2(M - M2), y = ex2(mk - M2);
+      L = L * x + lk * y;
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        const float4 v = ld4(r + hd * D + d0 + 64 * i);
+        o[i].x = o[i].x * x + v.x * y;
+        o[i].y = o[i].y * x + v.y * y;
+        o[i].z = o[i].z * x + v.z * y;
+        o[i].w = o[i].w * x + v.w * y;
+      }
+      M = M2;
+    };
+    auto finish = [&] {
+      if (hd >= nh) return;
+      const float r = M == -INFINITY ? 0.0f : 1.0f / L;  // no token behind any page: zeros
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+        store4(a.o.data,
+               b * a.o.row_stride + (static_cast<int64_t>(kvh) * a.group + h0 + hd) * a.o.head_stride + d0 + 64 * i,
+               a.o.dtype, make_float4(o[i].x * r, o[i].y * r, o[i].z * r, o[i].w * r));
+    };
+    reset();
+    for (int k = 0; k < kWarps; ++k)
+      add(reinterpret_cast<const float *>(ring) + k * S::Slot, [](const float *p) { return *p; },
+          [](const float *p) { return *reinterpret_cast<const float4 *>(p); });
+    const int64_t first = pre[b] * heads + pass * units, last = first + units - 1;  // units of this pass
+    if (first >= begin && last < end) {
+      finish();
+    } else {
+      // Part x starts at unit x * total / parts; the part that has unit v is ((v + 1) * parts - 1) / total.
+      const int64_t x0 = ((first + 1) * parts - 1) / total, x1 = ((last + 1) * parts - 1) / total;
+      float *slot = a.partials + (blockIdx.x * 2 + (cur == begin ? 0 : 1)) * int64_t(S::Slot);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) *reinterpret_cast<float4 *>(slot + hd * D + d0 + 64 * i) = o[i];
+      if ((tid & 15) == 0) {
+        slot[kHeads * D + hd] = M;
+        slot[kHeads * D + kHeads + hd] = L;
+      }
+      __threadfence();
+      __syncthreads();
+      unsigned *counter = a.counters + static_cast<int64_t>(b) * heads + pass;
+      if (tid == 0) flags[1] = atomicAdd(counter, 1u) == static_cast<unsigned>(x1 - x0);
+      __syncthreads();
+      if (flags[1]) {
+        __threadfence();
+        if (tid == 0) *counter = 0;
+        // Part x0 has this pass as its last segment (slot 1) unless it begins with it; the others
+        // begin with it. Parts follow one another in the workspace two slots apart.
+        const int64_t begin0 = x0 * total / parts;
+        reset();
+        for (int64_t x = x0; x <= x1; ++x)
+          add(a.partials + (x * 2 + (x == x0 && begin0 < first ? 1 : 0)) * int64_t(S::Slot),
+              [](const float *p) { return __ldcg(p); },
+              [](const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); });
+        finish();
+      }
+    }
+    // The next segment's copies (the async proxy) overwrite what was written and read here.
+    ptx::fence_proxy_async_smem();
+    __syncthreads();
+    cur += u_end - u_begin;
+    if (*abort) break;  // uniform: read behind a barrier, written before it
+  }
+  ptx::pdl_launch_dependents();
+}
+
+template <int D>
+size_t smem_bytes(int batch) {
+  using S = Shape<D>;
+  return static_cast<size_t>(kWarps) * kStages * S::Stage + 2 * S::NB * 32 * 16 + kWarps * kStages * 8 +
+         (kHeads * S::NB + kHeads + 4) * 4 + 8 * (static_cast<size_t>(batch) + 1);
+}
+
+template <int D>
+int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
+  auto kern = kv4_attn_kernel<D>;
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  std::call_once(once[dev.device], [&] {
+    err[dev.device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                           static_cast<int>(smem_bytes<D>(kKv4MaxBatch)));
+  });
+  if (err[dev.device] != cudaSuccess) return WOQ_ECUDA;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(dev.sm_count * kBlocksPerSm), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes<D>(a.batch);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return WOQ_ECUDA;
+  count_launches(1);
+  return WOQ_OK;
+}
+
+size_t counters_bytes(int32_t batch, int32_t kv_heads, int32_t group) {
+  const size_t n = static_cast<size_t>(batch) * kv_heads * ((group + kHeads - 1) / kHeads) * 4;
+  return (n + 255) & ~static_cast<size_t>(255);
+}
+
+}  // namespace
+
+size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int32_t dim, int sm_count) {
+  const size_t slot = (dim == 128 ? Shape<128>::Slot : Shape<64>::Slot) * sizeof(float);
+  return counters_bytes(batch, kv_heads, group) + static_cast<size_t>(sm_count) * kBlocksPerSm * 2 * slot;
+}
+
+int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, int32_t batch, const int32_t *table,
+                    int64_t width, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
+                    const DevInfo &dev) {
+  Args a;
+  a.q = q;
+  a.o = o;
+  a.codes = c.codes;
+  a.scales = reinterpret_cast<const uint8_t *>(c.scales);
+  a.lens = lens;
+  a.table = table;
+  a.pages = c.pages;
+  a.width = width;
+  a.batch = batch;
+  a.shift = __builtin_ctz(static_cast<unsigned>(c.page));
+  a.kv_heads = c.kv_heads;
+  a.group = q.heads / c.kv_heads;
+  a.chunks = (a.group + kHeads - 1) / kHeads;
+  a.scale = scale * 1.44269504088896340736f;
+  a.counters = static_cast<unsigned *>(workspace);
+  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
+                                         counters_bytes(batch, c.kv_heads, a.group));
+  const long long lim = wait_limit_cycles();
+  a.wait_limit = lim > 0 ? lim : kWaitLimit;
+  return c.dim == 128 ? launch<128>(a, s, dev) : launch<64>(a, s, dev);
+}
+
+int read_kv4_timeout_flag(int clear, unsigned *value) {
+  unsigned v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_kv4_timeout_flag, sizeof(v)) != cudaSuccess) return WOQ_ECUDA;
+  if (clear && v) {
+    const unsigned z = 0;
+    if (cudaMemcpyToSymbol(g_kv4_timeout_flag, &z, sizeof(z)) != cudaSuccess) return WOQ_ECUDA;
+  }
+  *value = v;
+  return WOQ_OK;
+}
+
+}  // namespace woq

@@ -69,6 +69,20 @@ int launch_gemv_chain(const woq_chain_item *items, int count, int64_t m, unsigne
                       cudaStream_t s, const DevInfo &dev);
 int read_chain_timeout_flag(int clear, unsigned *value);
 
+// ---- kv4.cu ----
+// kv4_append / kv4_gather (append == false: k and v are written). Arguments already validated.
+int launch_kv4_rows(const woq_kv4 &c, const woq_rows &k, const woq_rows &v, int64_t tokens, const int32_t *cu,
+                    const int32_t *start, int32_t batch, const int32_t *table, int64_t width, bool append,
+                    cudaStream_t s, const DevInfo &dev);
+
+// ---- kv4_attn.cu ----
+constexpr int kKv4MaxBatch = 4096;  // the kernel keeps a prefix sum over the sequences in shared memory
+size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int32_t dim, int sm_count);
+int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, int32_t batch, const int32_t *table,
+                    int64_t width, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
+                    const DevInfo &dev);
+int read_kv4_timeout_flag(int clear, unsigned *value);
+
 // ---- qgemm_tc.cu ----
 // How the tensor-core path runs a problem: tile width, K-splits and workspace layout
 // ([bf16 copy of X][FP32 partials of the splits], each 256-byte aligned).
