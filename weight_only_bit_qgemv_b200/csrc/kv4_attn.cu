@@ -5,19 +5,19 @@
 // Bound: memory. A token and key head is dim + dim / 8 bytes for 4 * dim * (query heads a key head)
 // flop; 144 bytes at dim 128. On the CUDA cores the unpacking and one multiply a query head would
 // already exceed what the bytes' time leaves, so both products run as warp matrix instructions
-// (mma.sync m16n8k16, binary16 in, FP32 out) on codes that never leave 4 bits as numbers: a nibble
-// under a mask IS a binary16 number, the subnormal u * 2^-24 (u = code + 8; u * 2^-20 for the
-// nibble above), which the tensor cores multiply exactly. Unpacking is one logic instruction for
-// two codes. tcgen05 would want the codes widened fourfold in shared memory first, and its 128 rows
-// would be 94 % empty at 8 query heads.
+// (mma.sync m16n8k16, binary16 in, FP32 out): two codes become two binary16 numbers with one logic
+// instruction and one exact subtraction. tcgen05 would want the codes widened fourfold in shared
+// memory first, and its 128 rows would be 94 % empty at 8 query heads.
 //
 // FP32 accuracy: the 16 rows of the left operand are 8 query heads' high binary16 parts and the
 // same heads' low parts, so that 22 bits of q, and then of p_j * vs[j, block], take part. The
-// query is scaled by a power of two into binary16's range, the weights likewise (see `room`). Per block
-// of 32 the key scale multiplies an FP32 block sum. The u = code + 8 offset is taken off by the sums'
-// starting values: -8 sum(q) for a key block, -8 sum(p vs), itself a product with a constant
-// operand, for a value block. Sums inside the matrix instructions run over 32 tokens at most; from
-// there on they are FP32 additions, rounded to nearest.
+// query is scaled by a power of two into binary16's range, the value scales likewise (see `room`). Per
+// block of 32 the key scale multiplies an FP32 block sum. Sums inside the matrix instructions, which cut
+// off what lies below their last bit, run over 32 tokens; from there on they are FP32 additions,
+// rounded to nearest. (A masked nibble is a binary16 as it stands, the subnormal u * 2^-24, and the offset
+// could be taken off the sums: measured, the matrix instructions then keep 18 bits instead of 26, as they
+// align subnormals as if they were 2^-14, and u >= 0 makes what they cut off a drift: 1.7e-4 of
+// the result at 115,000 tokens.)
 //
 // The left operand of the second product is the result of the first without leaving its registers.
 //
@@ -55,8 +55,9 @@ struct Shape {
   static constexpr int NB = D / 32;                   // blocks of a row
   static constexpr int RowBytes = D / 2;
   static constexpr int ScaleBytes = 4 * NB;           // of a token: key and value
-  static constexpr int Half = 16 * (2 * RowBytes + ScaleBytes);  // 16 tokens: keys, values, scales
-  static constexpr int Stage = 2 * Half;
+  static constexpr int Values = kUnit * RowBytes;     // a stage: keys, values, scales of 32 tokens
+  static constexpr int Scales = 2 * kUnit * RowBytes;
+  static constexpr int Stage = kUnit * (2 * RowBytes + ScaleBytes);
   static constexpr int Slot = kHeads * (D + 2);       // floats of a partial result
 };
 
@@ -85,9 +86,17 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint4 &a, uint32_t b0, 
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// Two codes of a word as u = code + 8 in binary16 subnormals: u * 2^-24, and u * 2^-20.
-__device__ __forceinline__ uint32_t low(uint32_t w) { return (w & 0x000f000fu) ^ 0x00080008u; }
-__device__ __forceinline__ uint32_t high(uint32_t w) { return (w & 0x00f000f0u) ^ 0x00800080u; }
+__device__ __forceinline__ __half2 h2(uint32_t w) { return *reinterpret_cast<const __half2 *>(&w); }
+__device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+
+// Two codes of a word as binary16: code, and 16 * code. The masked nibble with its sign bit turned
+// over (u = code + 8) and an exponent is 1024 + u (1024 + 16 u); the subtraction is exact.
+__device__ __forceinline__ uint32_t low(uint32_t w) {
+  return u32(__hsub2(h2((w & 0x000f000fu) ^ 0x64086408u), h2(0x64086408u)));
+}
+__device__ __forceinline__ uint32_t high(uint32_t w) {
+  return u32(__hsub2(h2((w & 0x00f000f0u) ^ 0x64806480u), h2(0x64806480u)));
+}
 
 // a and b as binary16 high parts and binary16 remainders: 22 bits of each.
 __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -107,12 +116,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   using S = Shape<D>;
   constexpr int NB = S::NB;
   extern __shared__ __align__(128) uint8_t smem[];
-  // [ring: kWarps * kStages * Stage][q operands: 2 NB * 32 * 16][bars][corr, fac][prefix]
+  // [ring: kWarps * kStages * Stage][q operands: 2 NB * 32 * 16][bars][fac, flags][prefix]
   uint8_t *ring = smem;
   uint4 *qop = reinterpret_cast<uint4 *>(smem + kWarps * kStages * S::Stage);
   uint64_t *bars = reinterpret_cast<uint64_t *>(qop + 2 * NB * 32);
-  float *corr = reinterpret_cast<float *>(bars + kWarps * kStages);  // [kHeads][NB]
-  float *fac = corr + kHeads * NB;                                   // [kHeads]
+  float *fac = reinterpret_cast<float *>(bars + kWarps * kStages);   // [kHeads]
   int *flags = reinterpret_cast<int *>(fac + kHeads);                // abort, last
   int64_t *pre = reinterpret_cast<int64_t *>(flags + 4);             // [batch + 1]: units before a sequence
 
@@ -179,50 +187,46 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       else hi = mid;
     }
     const int b = lo;
-    const int64_t units = pre[b + 1] - pre[b];
+    // a sequence has less than 2^31 tokens, so its units and their tokens fit 32 bits
+    const int units = static_cast<int>(pre[b + 1] - pre[b]);
     const int64_t at = cur - pre[b] * heads;
     const int pass = static_cast<int>(at / units);
-    const int64_t u_begin = at % units;
-    const int64_t u_end = u_begin + ((end - cur) < (units - u_begin) ? (end - cur) : (units - u_begin));
+    const int u_begin = static_cast<int>(at % units);
+    const int u_end = u_begin + static_cast<int>(end - cur < units - u_begin ? end - cur : units - u_begin);
     const int kvh = pass / a.chunks, h0 = (pass % a.chunks) * kHeads;
     const int nh = a.group - h0 < kHeads ? a.group - h0 : kHeads;
-    int64_t len = a.lens[b];
-    len = len > longest ? longest : len;
+    const int64_t len = a.lens[b] > longest ? longest : a.lens[b];
 
-    // One unit's copies into stage `st`, by lane 0. e0, e1: the table's entries for its halves.
+    // A unit's copies: lane 2 i + h of the first six has the 16 tokens of half h, i = 0 their keys,
+    // 1 values, 2 scales, and keeps the table's entries of its half for the units ahead.
+    const int half = lane & 1, what = lane >> 1;
     const int32_t *row = a.table + b * a.width;
-    auto entry = [&](int64_t u, int half) -> int32_t {
-      const int64_t key = u * kUnit + 16 * half;
+    const int page = 1 << a.shift;
+    const int unit_bytes = what == 2 ? S::ScaleBytes : S::RowBytes;
+    const int64_t page_bytes = int64_t(a.kv_heads) * page * (what == 2 ? S::ScaleBytes : 2 * S::RowBytes);
+    const uint8_t *pool = what == 2 ? a.scales + int64_t(kvh) * page * S::ScaleBytes
+                                    : a.codes + (int64_t(kvh) * 2 + what) * page * S::RowBytes;
+    uint8_t *into = mine + what * S::Values + 16 * half * unit_bytes;
+    auto entry = [&](int u) -> int32_t {
+      const int64_t key = int64_t(u) * kUnit + 16 * half;
       return u < u_end && key < len ? row[key >> a.shift] : -1;
     };
     auto good = [&](int32_t e) { return e >= 0 && e < a.pages; };
-    auto issue = [&](int64_t u, int st, int32_t e0, int32_t e1) {
-      if (lane != 0 || u >= u_end) return;
-      const uint32_t bytes = (good(e0) ? S::Half : 0) + (good(e1) ? S::Half : 0);
-      ptx::mbar_arrive_expect_tx(&bar[st], bytes);
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int32_t e = half ? e1 : e0;
-        if (!good(e)) continue;
-        const int64_t page = int64_t(1) << a.shift;
-        const int64_t slot = (u * kUnit + 16 * half) & (page - 1);
-        const int64_t head = static_cast<int64_t>(e) * a.kv_heads + kvh;
-        uint8_t *dst = mine + st * S::Stage + half * S::Half;
-        ptx::bulk_load(dst, a.codes + (head * 2 * page + slot) * S::RowBytes, 16 * S::RowBytes, &bar[st]);
-        ptx::bulk_load(dst + 16 * S::RowBytes, a.codes + ((head * 2 + 1) * page + slot) * S::RowBytes,
-                       16 * S::RowBytes, &bar[st]);
-        ptx::bulk_load(dst + 32 * S::RowBytes, a.scales + (head * page + slot) * S::ScaleBytes,
-                       16 * S::ScaleBytes, &bar[st]);
+    auto issue = [&](int u, int st, int32_t e) {
+      const uint32_t halves = __popc(__ballot_sync(0xffffffffu, good(e)) & 3u);
+      if (u >= u_end) return;
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&bar[st], halves * (S::Stage / 2));
+      if (lane < 6 && good(e)) {
+        const uint32_t slot = (static_cast<uint32_t>(u) * kUnit + 16 * half) & (page - 1);
+        ptx::bulk_load(into + st * S::Stage, pool + e * page_bytes + slot * unit_bytes, 16 * unit_bytes, &bar[st]);
       }
     };
-    const int64_t u0 = u_begin + warp;
-    int32_t e[kStages + 1][2];  // entries of the units in the ring and of the one after
+    const int u0 = u_begin + warp;
+    int32_t e[kStages + 1];  // entries of the units in the ring and of the one after
 #pragma unroll
-    for (int s = 0; s <= kStages; ++s)
+    for (int i = 0; i <= kStages; ++i) e[i] = entry(u0 + i * kWarps);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) e[s][h] = entry(u0 + s * kWarps, h);
-#pragma unroll
-    for (int s = 0; s < kStages; ++s) issue(u0 + s * kWarps, s, e[s][0], e[s][1]);
+    for (int i = 0; i < kStages; ++i) issue(u0 + i * kWarps, i, e[i]);
 
     // The query: rows h0 .. h0 + nh - 1 of this key head, times scale * log2(e), times the power of two
     // that brings the row's largest into [2^13, 2^14).
@@ -250,10 +254,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         v[i] *= up;
-        float sum = v[i];
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        if (lane == 0) corr[r * NB + i] = sum * (-8.0f / 16777216.0f);
         // Element `lane` = 8 tt + n of the block: matrix step 2 i + (n / 2 % 2), a or second pair by n % 2,
         // first or second of the pair by n / 4; odd n meet codes 16 times too large.
         const int n = lane & 7, tt = lane >> 3;
@@ -265,20 +265,19 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         dst[0] = h;  // .x / .z: high parts (rows 0..7)
         dst[2] = l;  // .y / .w: low parts (rows 8..15)
       }
-      if (lane == 0) fac[r] = ldexpf(1.0f, 24 + ex);
+      if (lane == 0) fac[r] = ldexpf(1.0f, ex);
     }
     __syncthreads();
 
-    float kc[NB];
-#pragma unroll
-    for (int i = 0; i < NB; ++i) kc[i] = corr[g * NB + i];
     const float f = fac[g];
 
     float m = -INFINITY;  // running maximum of the scores (log2), shared by the quad
     float l = 0;          // this lane's sum of p
-    // p = 2^(s - m + room): the power 2^room lifts p * vs to the middle of binary16's range, so that
-    // what lies below its smallest number is below 2^-28 of the largest. It cancels in o / sum(p).
-    float room = 0, limit = -1;
+    // p is taken times 2^6 and the value scales times 2^room: p * vs then reaches at least 1, so that
+    // binary16's smallest step is below 2^-24 of the largest. The first cancels in o / sum(p).
+    int room = 0;
+    float most = 0;  // the largest scale that room allows
+    int limit = -1;  // its bits as binary16
     float2 acc[NB][4];  // value block, n-tile: columns of tokens' head g, dims 32 b + 8 t + i and + 4
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -287,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 
     int st = 0;
     bool ok = true;
-    for (int64_t u = u0; u < u_end; u += kWarps) {
+    for (int u = u0; u < u_end; u += kWarps) {
       if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(&bar[st], phases >> st & 1, a.wait_limit, abort))) {
         *abort = 1;
         atomicOr(&g_kv4_timeout_flag, 1u);
@@ -297,17 +296,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       phases ^= 1u << st;
       const uint8_t *base = mine + st * S::Stage;
 
+      // Tokens of each half that are there: all 32, as a rule.
+      const uint32_t pages_ok = __ballot_sync(0xffffffffu, good(e[0])) & 3u;
+      const int64_t rest = len - int64_t(u) * kUnit;
+      const bool full = pages_ok == 3u && rest >= kUnit;
+
       // ---- scores: two matrices of 8 tokens for each half of the unit ----
       float2 s[2][2];
       uint32_t vs[2][2][2][NB / 2];  // value scales: half, matrix, token, pairs of blocks
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint8_t *hb = base + h * S::Half;
-        const bool page_ok = good(e[0][h]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           // column g of the matrix is token 8 i + (g / 2) + 4 (g % 2)
-          const uint8_t *kr = hb + token_of(i, g >> 1, g & 1) * S::RowBytes + t * (4 * NB);
+          const uint8_t *kr = base + (16 * h + token_of(i, g >> 1, g & 1)) * S::RowBytes + t * (4 * NB);
           uint32_t w[NB];
           if constexpr (NB == 4) {
             const uint4 x = *reinterpret_cast<const uint4 *>(kr);
@@ -316,28 +318,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
             const uint2 x = *reinterpret_cast<const uint2 *>(kr);
             w[0] = x.x; w[1] = x.y;
           }
-          // scales of this lane's two tokens, 0 where there is no token
-          uint32_t ks[2][NB / 2];
-          bool live[2];
+          uint32_t ks[2][NB / 2];  // scales of this lane's two tokens
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int tok = token_of(i, t, j);
-            live[j] = page_ok && u * kUnit + 16 * h + tok < len;
-            const uint8_t *sr = hb + 32 * S::RowBytes + tok * S::ScaleBytes;
+            const uint8_t *sr = base + S::Scales + (16 * h + token_of(i, t, j)) * S::ScaleBytes;
             if constexpr (NB == 4) {
               const uint4 x = *reinterpret_cast<const uint4 *>(sr);
               ks[j][0] = x.x; ks[j][1] = x.y;
-              vs[h][i][j][0] = live[j] ? x.z : 0; vs[h][i][j][1] = live[j] ? x.w : 0;
+              vs[h][i][j][0] = x.z; vs[h][i][j][1] = x.w;
             } else {
               const uint2 x = *reinterpret_cast<const uint2 *>(sr);
               ks[j][0] = x.x;
-              vs[h][i][j][0] = live[j] ? x.y : 0;
+              vs[h][i][j][0] = x.y;
             }
           }
           float2 sum = make_float2(0, 0);
 #pragma unroll
           for (int k = 0; k < NB; ++k) {
-            float c[4] = {kc[k], kc[k], 0, 0};
+            float c[4] = {0, 0, 0, 0};
             mma(c, qop[(2 * k) * 32 + lane], low(w[k]), high(w[k]), c);
             const uint32_t w8 = w[k] >> 8;
             mma(c, qop[(2 * k + 1) * 32 + lane], low(w8), high(w8), c);
@@ -347,13 +345,27 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
                                           k & 1 ? __high2float(s1) : __low2float(s1));
             sum = __ffma2_rn(__fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])), sc, sum);
           }
-          sum = __fmul2_rn(sum, make_float2(f, f));
-          s[h][i] = make_float2(live[0] ? sum.x : -INFINITY, live[1] ? sum.y : -INFINITY);
+          s[h][i] = __fmul2_rn(sum, make_float2(f, f));
         }
       }
+      if (!full) {  // warp-uniform: tokens that are not there weigh nothing, whatever the stage holds
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              if (!(pages_ok >> h & 1) || 16 * h + token_of(i, t, j) >= rest) {
+                (j ? s[h][i].y : s[h][i].x) = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < NB / 2; ++k) vs[h][i][j][k] = 0;
+              }
+      }
 
-      // ---- largest value scale: keep p * vs inside binary16 ----
-      __half2 big = __float2half2_rn(0);
+      // ---- value scales: keep p * vs inside binary16 ----
+      // Compared as 16-bit numbers, which order binary16 of one sign; a negative scale (kv4_append
+      // writes none) counts as large and only takes the longer way.
+      uint32_t big = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -361,19 +373,45 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < NB / 2; ++k)
-              big = __hmax2(big, __habs2(*reinterpret_cast<const __half2 *>(&vs[h][i][j][k])));
-      const float most = fmaxf(__low2float(big), __high2float(big));
+            for (int k = 0; k < NB / 2; ++k) big = __vmaxu2(big, vs[h][i][j][k]);
       float shift = 0;  // change of room
-      if (__any_sync(0xffffffffu, most > limit)) {
-        float all = most;
+      if (__any_sync(0xffffffffu, static_cast<int>(max(big & 0xffffu, big >> 16)) > limit)) {
+        __half2 m2 = __float2half2_rn(0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < NB / 2; ++k) m2 = __hmax2(m2, __habs2(h2(vs[h][i][j][k])));
+        float all = fmaxf(__low2float(m2), __high2float(m2));
 #pragma unroll
         for (int i = 1; i < 32; i <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
-        // largest p * vs below 2^4 now, up to 2^15 (limit) before room changes again
-        const float next = all > 0 && all < INFINITY ? 3.0f - static_cast<float>(ilogbf(all)) : 0.0f;
-        shift = next - room;
-        room = next;
-        limit = ldexpf(1.0f, 15 - static_cast<int>(next));
+        if (limit < 0 || all > most) {
+          // Scales from 2^-6 to 2^4 are taken as they are, others times a power of two that brings the
+          // largest to [1, 2); they may grow to 2^8 before this changes again.
+          const int ex = all > 0 && all < INFINITY ? ilogbf(all) : 0;
+          const int next = ex < -6 || ex > 3 ? -ex : 0;
+          shift = static_cast<float>(next - room);
+          room = next;
+          most = ldexpf(1.0f, 8 - next);
+          limit = __half_as_ushort(__float2half_rz(fminf(most, 65504.0f)));
+        }
+      }
+      if (room != 0) {  // warp-uniform
+        // in two steps, as 2^24 is no binary16; each product is exact or, far below the largest, rounded
+        const __half2 a1 = __float2half2_rn(ldexpf(1.0f, room / 2));
+        const __half2 a2 = __float2half2_rn(ldexpf(1.0f, room - room / 2));
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int k = 0; k < NB / 2; ++k)
+                vs[h][i][j][k] = u32(__hmul2(__hmul2(h2(vs[h][i][j][k]), a1), a2));
       }
 
       // ---- softmax over the unit ----
@@ -383,12 +421,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // Any token makes the maximum finite, so that -infinity means that there was none: a row of
       // scores that are all NaN or -infinity gives NaN, as the formula does.
-      if (good(e[0][0]) || good(e[0][1])) mx = fmaxf(mx, -3.402823466e38f);
+      if (pages_ok) mx = fmaxf(mx, -3.402823466e38f);
       const float m2 = fmaxf(m, mx);
-      const float ref = (m2 == -INFINITY ? 0.0f : m2) - room;
-      const float alpha = ex2((m == -INFINITY ? -INFINITY : m - (m2 - shift)));
+      const float ref = (m2 == -INFINITY ? 0.0f : m2) - 6.0f;
+      const float beta = m == -INFINITY ? -INFINITY : m - m2;
+      const float alpha = ex2(beta + shift);
+      l *= ex2(beta);
       m = m2;
-      l *= alpha;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -399,6 +438,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 
       // ---- values ----
       const float2 al = make_float2(alpha, alpha);
+      uint32_t ph[2][2], pl[2][2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split(s[h][i].x, s[h][i].y, ph[h][i], pl[h][i]);
 #pragma unroll
       for (int kp = 0; kp < NB / 2; ++kp) {  // pairs of blocks: one word of a lane's codes
         uint32_t v[2][2][2];  // half, matrix, block of the pair: two tokens' four codes
@@ -406,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const uint8_t *vr = base + h * S::Half + 16 * S::RowBytes + g * (2 * NB) + kp * 4;
+            const uint8_t *vr = base + S::Values + 16 * h * S::RowBytes + g * (2 * NB) + kp * 4;
             const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 0) * S::RowBytes);
             const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 1) * S::RowBytes);
             v[h][i][0] = __byte_perm(w0, w1, 0x5410);
@@ -418,29 +462,24 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
           uint4 p[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float2 x[2];
+            // (ph + pl) * vs as a sum of two binary16 again: the product's rounding error is itself a
+            // binary16, which the fused multiply-add gives exactly
+            uint32_t x[2], y[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const __half2 s0 = *reinterpret_cast<const __half2 *>(&vs[h][i][0][kp]);
-              const __half2 s1 = *reinterpret_cast<const __half2 *>(&vs[h][i][1][kp]);
-              x[i] = __fmul2_rn(s[h][i], make_float2(kb ? __high2float(s0) : __low2float(s0),
-                                                     kb ? __high2float(s1) : __low2float(s1)));
+              const __half2 sc = h2(__byte_perm(vs[h][i][0][kp], vs[h][i][1][kp], kb ? 0x7632 : 0x5410));
+              const __half2 hi = __hmul2(h2(ph[h][i]), sc);
+              x[i] = u32(hi);
+              y[i] = u32(__hfma2(h2(pl[h][i]), sc, __hfma2(h2(ph[h][i]), sc, __hneg2(hi))));
             }
-            split(x[0].x, x[0].y, p[h].x, p[h].y);
-            split(x[1].x, x[1].y, p[h].z, p[h].w);
+            p[h] = make_uint4(x[0], y[0], x[1], y[1]);
           }
-          // -8 sum(p vs) in the units of the codes' two places
-          float c1[4] = {0, 0, 0, 0}, c16[4] = {0, 0, 0, 0};
-          mma(c1, p[0], 0x80088008u, 0x80088008u, c1);
-          mma(c1, p[1], 0x80088008u, 0x80088008u, c1);
-          mma(c16, p[0], 0x80808080u, 0x80808080u, c16);
-          mma(c16, p[1], 0x80808080u, 0x80808080u, c16);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float c[4];
+            float c[4] = {0, 0, 0, 0};
             const int sh = 8 * (i >> 1);
             auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh) : low(w >> sh); };
-            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), i & 1 ? c16 : c1);
+            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), c);
             mma(c, p[1], pick(v[1][0][kb]), pick(v[1][1][kb]), c);
             acc[k][i] = __ffma2_rn(acc[k][i], al, __fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
           }
@@ -448,12 +487,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       }
 
       __syncwarp();  // every lane has read the stage
-      e[0][0] = e[1][0]; e[0][1] = e[1][1];
 #pragma unroll
-      for (int i = 1; i < kStages; ++i) { e[i][0] = e[i + 1][0]; e[i][1] = e[i + 1][1]; }
-      issue(u + kStages * kWarps, st, e[kStages - 1][0], e[kStages - 1][1]);
-      e[kStages][0] = entry(u + (kStages + 1) * kWarps, 0);
-      e[kStages][1] = entry(u + (kStages + 1) * kWarps, 1);
+      for (int i = 0; i < kStages; ++i) e[i] = e[i + 1];
+      issue(u + kStages * kWarps, st, e[kStages - 1]);
+      e[kStages] = entry(u + (kStages + 1) * kWarps);
       st = st + 1 == kStages ? 0 : st + 1;
     }
     if (!ok) {
@@ -467,16 +504,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     __syncthreads();  // the ring is idle: it takes the warps' results
     float *res = reinterpret_cast<float *>(ring) + warp * S::Slot;
-    // m as the reference that p was taken against
     if (t == 0) {
-      res[kHeads * D + g] = m == -INFINITY ? -INFINITY : m - room;
+      res[kHeads * D + g] = m;
       res[kHeads * D + kHeads + g] = l;
     }
 #pragma unroll
     for (int k = 0; k < NB; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float unit = i & 1 ? 1048576.0f : 16777216.0f;  // 2^20, 2^24
+        const float unit = ldexpf(i & 1 ? 0.0625f : 1.0f, -room);
         res[g * D + 32 * k + 8 * t + i] = acc[k][i].x * unit;
         res[g * D + 32 * k + 8 * t + 4 + i] = acc[k][i].y * unit;
       }
@@ -568,7 +604,7 @@ template <int D>
 size_t smem_bytes(int batch) {
   using S = Shape<D>;
   return static_cast<size_t>(kWarps) * kStages * S::Stage + 2 * S::NB * 32 * 16 + kWarps * kStages * 8 +
-         (kHeads * S::NB + kHeads + 4) * 4 + 8 * (static_cast<size_t>(batch) + 1);
+         (kHeads + 4) * 4 + 8 * (static_cast<size_t>(batch) + 1);
 }
 
 template <int D>
