@@ -326,7 +326,8 @@ int qgemm_bf16_noalloc(const float *X, int64_t m, const woq_weight *w, float *Y,
 
 /*
  * Attention: what a decoder layer does between its packed projections. A 4-bit cache of keys and
- * values (kv4_append, kv4_gather) and one-token attention over it (kv4_attn).
+ * values (kv4_append, kv4_gather) and one-token attention over it (kv4_attn), and attention over
+ * whole prompts (attn_prompt).
  *
  * Activations are float32 as everywhere in this library; these calls also take binary16 and
  * bfloat16 ones. Whatever the type, scores, softmax and sums are FP32.
@@ -397,6 +398,33 @@ int kv4_append(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64
  */
 int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, int32_t batch, const int32_t *table,
                int64_t width, int64_t tokens, const woq_rows *k, const woq_rows *v, void *stream);
+
+/*
+ * attn_prompt -- causal attention over whole prompts, packed sequence after sequence: for rows
+ * cu[b] <= i < cu[b + 1] and query head h, with key head h / (q.heads / k.heads),
+ * o[i, h] = sum_{j = cu[b]..i} p_j v[j],  p = softmax_j(scale * q[i, h] . k[j]).
+ *   q, o    device, [tokens, q.heads, dim];  k, v device, [tokens, k.heads, dim], all of one type.
+ *           q.heads a multiple of k.heads, at most 32768; k.heads at most 1024; dim 64 or 128. o
+ *           overlaps none of the others. Slices of one fused projection are fine.
+ *   cu      device, int32 [batch + 1], non-decreasing; sequences may be empty. Rows before cu[0] and
+ *           from cu[batch] on are not written, and have no influence
+ *   scale   positive and finite, usually dim^-1/2
+ *   workspace  device, 256-byte aligned, attn_prompt_workspace_bytes(...) bytes (0 for 16-bit types);
+ *           its contents on entry do not matter; calls that share one must be ordered on one stream
+ * float32: q, k and v as two binary16 planes each, 22 significant bits of every value within 2^17 of the
+ * largest of its row (q) or of its 64 tokens of one head (k, v), three products on the tcgen05 tensor cores, FP32
+ * sums. 16-bit: operands as they are, weights rounded to the type. The lengths stay on the device; the grid
+ * goes by tokens and batch. Deterministic. A value that is not finite enters only rows that see it: a
+ * row that sees such a q or k is NaN, one that sees such a v is not finite in its column.
+ * batch 1 to 2^20; (tokens / 256 + batch) * q.heads < 2^31.
+ * Errors: WOQ_EINVAL (null pointers, dtypes, heads, batch, scale, overlap), WOQ_ESHAPE (dim, sizes, strides),
+ * WOQ_EALIGN, WOQ_EWORKSPACE, WOQ_EDEVICE, WOQ_ECUDA. Waits inside the kernel are bounded, as qgemm's.
+ */
+size_t attn_prompt_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                   int32_t dtype);
+int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+                int32_t batch, int32_t dim, float scale, const woq_rows *o, void *workspace,
+                size_t workspace_bytes, void *stream);
 
 /*
  * kv4_attn -- a decode step's attention: for each sequence b and query head h, with key head

@@ -92,6 +92,39 @@ def test_attention_refusals():
     assert side in (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE) or torch.cuda.is_available()
 
 
+def test_prompt_refusals():
+    L = _lib.lib()
+
+    def call(q=None, k=None, v=None, o=None, tokens=4, cu=OK, batch=1, dim=128, scale=0.1, ws=1 << 21, n=1 << 30):
+        args = [q or rows(heads=4, row=512), k or rows(data=FAR), v or rows(data=2 * FAR),
+                o or rows(data=3 * FAR, heads=4, row=512)]
+        q, k, v, o = (ctypes.byref(x) for x in args)
+        return L.attn_prompt(q, k, v, tokens, cu, batch, dim, scale, o, ws, n, None)
+
+    for r, want in BAD_ROWS:
+        assert call(k=r) in (want, _lib.WOQ_EINVAL) and call(v=r) in (want, _lib.WOQ_EINVAL)
+    assert call(q=rows(heads=3)) == call(o=rows(heads=2)) == call(v=rows(heads=1)) == _lib.WOQ_EINVAL
+    assert call(k=rows(heads=1025, row=1025 * 128), q=rows(heads=1025, row=1025 * 128)) == _lib.WOQ_EINVAL
+    for name in ("q", "k", "v", "o"):  # one type for all
+        r = rows(data=5 * FAR, dtype=2, heads=4 if name in "qo" else 2, row=512)
+        assert call(**{name: r}) == _lib.WOQ_EINVAL
+    assert call(dim=96) == call(dim=32) == _lib.WOQ_ESHAPE
+    for scale in (0.0, -1.0, math.inf, math.nan):
+        assert call(scale=scale) == _lib.WOQ_EINVAL
+    assert call(tokens=-1) == call(cu=None) == call(batch=0) == call(batch=2**20 + 1) == _lib.WOQ_EINVAL
+    assert call(tokens=2**31) == _lib.WOQ_ESHAPE and call(cu=OK + 2) == _lib.WOQ_EALIGN
+    many = rows(data=4 * FAR, heads=32768, row=32768 * 128)
+    assert call(q=many, o=rows(data=8 * FAR, heads=32768, row=32768 * 128), tokens=2**25) == _lib.WOQ_ESHAPE
+    assert call(ws=None) == call(n=1024) == _lib.WOQ_EWORKSPACE and call(ws=(1 << 21) + 64) == _lib.WOQ_EALIGN
+    for name in ("q", "k", "v"):  # the output on an input
+        r = rows(data=3 * FAR, heads=4 if name == "q" else 2, row=512)
+        assert call(**{name: r}) == _lib.WOQ_EINVAL
+    size = L.attn_prompt_workspace_bytes
+    assert size(100, 1, 4, 2, 128, _lib.WOQ_BF16) == 0 and size(100, 1, 4, 2, 128, _lib.WOQ_F32) > 100 * 8 * 128 * 4
+    for bad in ((-1, 1, 4, 2, 128, 0), (100, 0, 4, 2, 128, 0), (100, 1, 3, 2, 128, 0), (100, 1, 4, 2, 96, 0)):
+        assert size(*bad) == 0
+
+
 def test_workspace_sizes():
     L = _lib.lib()
     size = L.kv4_attn_workspace_bytes
@@ -110,8 +143,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     assert (cache.kv_heads, cache.dim, cache.page) == (1, 128, 16) and cache.nbytes == 16 * 144
     x, i = torch.zeros(1, 1, 128), torch.zeros(2, dtype=torch.int32)
     for call in (lambda: woq.kv4_append(cache, x, x, i, i[None]), lambda: woq.kv4_attn(x, cache, i[:1], i[None, :1]),
+                 lambda: woq.attn_prompt(x, x, x, i), lambda: woq.attn_prompt_workspace(x[0], x, 1),
                  lambda: woq.kv4_gather(cache, i, i[None], k_out=x, v_out=x), lambda: woq.kv4_gather(cache, i, i[None])):
         with pytest.raises(ValueError):
             call()
-    for name in ("kv4_append", "kv4_gather", "kv4_attn", "KV4Cache"):
+    for name in ("attn_prompt", "kv4_append", "kv4_gather", "kv4_attn", "KV4Cache"):
         assert name in woq.__all__

@@ -1,0 +1,230 @@
+"""attn_prompt against causal attention in 64 bits."""
+
+import numpy as np
+import pytest
+import torch
+
+import weight_only_bit_qgemv_b200 as woq
+from weight_only_bit_qgemv_b200 import _lib
+from tests import attn_ref as ref
+
+pytestmark = pytest.mark.gpu
+TYPES = [torch.float32, torch.float16, torch.bfloat16]
+
+
+def ints(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def fused(seed, tokens, heads, kv, dim, dtype):
+    """Slices of one projection's rows: queries, keys, values."""
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(tokens, heads + 2 * kv, dim, generator=g).to(dtype).cuda()
+    return x[:, :heads], x[:, heads:heads + kv], x[:, heads + kv:]
+
+
+def exact(q, k, v, cu, scale):
+    """(result, its tolerance) in float64, on the GPU: rows of no sequence are 0 with tolerance 0."""
+    dtype, heads, group = q.dtype, q.shape[1], q.shape[1] // k.shape[1]
+    q, k, v = (x.double() for x in (q, k, v))
+    out, tol = torch.zeros_like(q), torch.zeros_like(q)
+    products = 22 if dtype == torch.float32 else 60  # 16-bit operands take part as they are
+    weight = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
+    for a, b in zip(cu[:-1], cu[1:]):
+        for h in range(heads):
+            kh, vh = k[a:b, h // group], v[a:b, h // group]
+            for i in range(a, b, 2048):
+                j = min(b, i + 2048)
+                x = q[i:j, h] @ kh[:j - a].T * scale
+                seen = torch.arange(j - a, device="cuda") <= torch.arange(i - a, j - a, device="cuda")[:, None]
+                p = torch.softmax(x.masked_fill(~seen, -torch.inf), -1)
+                out[i:j, h] = p @ vh[:j - a]
+                # ref.tolerance's derivation, with sums over what a row sees: FP32 sums of a score's 2^7 terms add
+                # 2^-17 of sum |q k| at most (rounding to nothing, 2^-24 a step), a rounded weight half a step of
+                # it on either side of the quotient
+                e = (2.0 ** (2 - products) + 2.0**-17) * (q[i:j, h].abs() @ kh[:j - a].abs().T * scale)
+                e = e.masked_fill(~seen, 0).amax(-1, keepdim=True)
+                tol[i:j, h] = (2 * e + 2.0**-18 + 2 * weight) * (p @ vh[:j - a].abs())
+                # weights of up to 2^-25 of the largest are lost in binary16, and its subnormals' steps
+                tol[i:j, h] += (2.0**-25 if dtype == torch.float16 else 0.0) * seen.sum(-1, keepdim=True) * vh.abs().max()
+    unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
+    return out, tol + unit * out.abs() + (6e-8 if dtype == torch.float16 else 0.0)
+
+
+def check(q, k, v, cu, scale=None, **kw):
+    out = woq.attn_prompt(q, k, v, ints(cu), scale=scale, **kw)
+    want, tol = exact(q, k, v, cu, q.shape[2] ** -0.5 if scale is None else scale)
+    for a, b in zip(cu[:-1], cu[1:]):
+        err = (out[a:b].double() - want[a:b]).abs()
+        assert (err <= tol[a:b]).all(), ((a, b), err.max().item(), (err - tol[a:b]).max().item())
+    assert woq.device_status() == _lib.WOQ_OK
+    return out
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("heads,kv,dim,lens", [
+    (1, 1, 64, [1]),
+    (1, 1, 128, [2]),
+    (2, 1, 128, [63, 64, 65, 0, 127, 128, 129]),          # around the tiles of keys and rows
+    (4, 4, 64, [255, 256, 257, 0, 0, 1]),
+    (6, 2, 128, [700, 3]),
+    (16, 8, 128, [137]),
+    (5, 1, 64, [383, 385, 511, 513]),
+    (8, 1, 128, [1030]),
+])
+def test_matches_the_formula(dtype, heads, kv, dim, lens):
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    q, k, v = fused(heads + dim + len(lens), cu[-1], heads, kv, dim, dtype)
+    check(q, k, v, cu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_long_prompts(dtype):
+    cu = [0, 4999, 5000, 9201]
+    q, k, v = fused(3, cu[-1], 2, 1, 128, dtype)
+    check(q, k, v, cu)
+
+
+def test_many_short_sequences():
+    """More sequences than one pass over their ends holds, most of them of a few rows."""
+    lens = [(i * 37) % 19 for i in range(200)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    q, k, v = fused(4, cu[-1], 2, 2, 64, torch.float32)
+    check(q, k, v, cu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_rows_outside_the_sequences(dtype):
+    """Rows before, behind and between hold NaN: they are not written and have no influence."""
+    cu = [5, 5 + 130, 5 + 130 + 20]
+    q, k, v = fused(5, 170, 4, 2, 128, dtype)
+    for x in (q, k, v):
+        x[:5] = float("nan")
+        x[155:] = float("inf")
+    out = torch.full((170, 4, 128), 7.0, dtype=dtype, device="cuda")
+    check(q, k, v, cu, out=out)
+    assert (out[:5] == 7).all() and (out[155:] == 7).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("at", [0, 100, 131, 255, 300])
+def test_values_that_are_not_finite_enter_only_rows_that_see_them(dtype, at):
+    cu = [0, 301, 420]
+    q, k, v = fused(6, 420, 4, 2, 64, dtype)
+    clean = woq.attn_prompt(q, k, v, ints(cu))
+    v2 = v.clone()
+    v2[at, 0, 9], v2[at, 1, 3] = float("nan"), float("inf")
+    out = woq.attn_prompt(q, k, v2, ints(cu))
+    hit = torch.zeros(420, 4, 64, dtype=torch.bool, device="cuda")
+    hit[at:301, :2, 9] = True
+    hit[at:301, 2:, 3] = True
+    assert torch.equal(~out.isfinite(), hit)
+
+    def same():
+        # float32: what is not finite has no part in its tile's power of two, so bits below 2^-22 may move
+        if dtype != torch.float32:
+            return torch.equal(out[~hit], clean[~hit])
+        return (out[~hit] - clean[~hit]).abs().max() <= 2.0**-16 * v.abs().max()
+
+    assert same()
+    assert out[at, 2, 3] == float("inf")
+    # keys and queries: rows that see one are NaN as a whole, the others as they were
+    k2 = k.clone()
+    k2[at, 0, 1] = float("nan")
+    out = woq.attn_prompt(q, k2, v, ints(cu))
+    hit[:] = False
+    hit[at:301, :2] = True
+    assert torch.equal(out.isnan(), hit) and same()
+    q2 = q.clone()
+    q2[at, 1, 5] = float("nan")
+    out = woq.attn_prompt(q2, k, v, ints(cu))
+    hit[:] = False
+    hit[at, 1] = True
+    assert torch.equal(out.isnan(), hit) and same()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_scores_far_apart_and_sizes_far_from_one(dtype):
+    cu = [0, 400, 600]
+    q, k, v = fused(7, 600, 4, 2, 128, dtype)
+    check(q * 30, k, v, cu)                       # one key has nearly all the weight
+    check(q, k, v, cu, scale=1e-4)                # all keys weigh the same
+    check(torch.zeros_like(q), k, v, cu)
+    if dtype == torch.float32:
+        check(q * 1e-18, k * 1e18, v * 1e-25, cu)
+        check(q * 1e12, k * 1e-12, v * 1e30, cu)
+        grow = torch.logspace(-6, 6, 600, device="cuda")[:, None, None]
+        check(q / grow, k, v * grow, cu)          # each tile with powers of two of its own
+    if dtype == torch.bfloat16:
+        check(q, k, v * 1e30, cu)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_one_key_far_above_the_others(dtype):
+    """Row maxima that rise late: what was summed before is scaled down to nothing."""
+    q, k, v = fused(8, 520, 2, 1, 64, dtype)
+    k = k.clone()
+    k[300] = q[300, :1] * 6
+    check(q, k, v, [0, 520])
+
+
+def test_strides_and_neighbours():
+    q, k, v = fused(9, 300, 6, 3, 128, torch.float32)
+    wide = torch.full((300, 10, 160), 7.0, device="cuda")
+    check(q, k, v, [0, 300], out=wide[:, 2:8, 16:144])
+    assert (wide[:, :2] == 7).all() and (wide[:, 8:] == 7).all()
+    assert (wide[..., :16] == 7).all() and (wide[..., 144:] == 7).all()
+    heads_first = q.transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(woq.attn_prompt(heads_first, k, v, ints([0, 300])), wide[:, 2:8, 16:144])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_same_bits_every_time_captured_and_on_another_stream(dtype):
+    cu = ints([0, 700, 900])
+    q, k, v = fused(10, 900, 4, 2, 128, dtype)
+    want = woq.attn_prompt(q, k, v, cu)
+    for _ in range(3):
+        assert torch.equal(woq.attn_prompt(q, k, v, cu), want)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = woq.attn_prompt(q, k, v, cu, stream=side, out=torch.zeros_like(want))
+    side.synchronize()
+    assert torch.equal(got, want)
+    ws, out = woq.attn_prompt_workspace(q, k, 2), torch.zeros_like(want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        woq.attn_prompt(q, k, v, cu, out=out, workspace=ws)
+        woq.attn_prompt(q, k, v, cu, out=out, workspace=ws)  # shares the workspace, ordered behind it
+    for ends in ([0, 700, 900], [0, 1, 900], [10, 450, 451]):  # other lengths in the same graph
+        cu.copy_(ints(ends))
+        out.zero_()
+        graph.replay()
+        assert torch.equal(out, woq.attn_prompt(q, k, v, cu))
+
+
+def test_more_tokens_than_the_sequences_have_and_ends_out_of_order():
+    q, k, v = fused(11, 500, 2, 1, 64, torch.float32)
+    out = woq.attn_prompt(q, k, v, ints([0, 0, 0]))
+    assert not out.any()
+    # ends that are no ends: nothing outside the rows is read or written, and a good sequence is right
+    out = torch.full((600, 2, 64), 7.0, device="cuda")
+    woq.attn_prompt(q, k, v, ints([0, 100, -5, 2**31 - 1, 50]), out=out[:500])
+    assert (out[500:] == 7).all() and woq.device_status() == _lib.WOQ_OK
+
+
+def test_a_stuck_wait_gives_up_and_the_context_survives():
+    q, k, v = fused(12, 300, 2, 1, 128, torch.float32)
+    want = woq.attn_prompt(q, k, v, ints([0, 300]))
+    L = _lib.lib()
+    assert woq.device_status(clear=True) == _lib.WOQ_OK
+    try:
+        L.woq_debug_set_wait_limit(-200000)
+        woq.attn_prompt(q, k, v, ints([0, 300]))
+        assert woq.device_status(clear=True) == _lib.WOQ_ETIMEOUT
+    finally:
+        L.woq_debug_set_wait_limit(0)
+    assert torch.equal(woq.attn_prompt(q, k, v, ints([0, 300])), want)
+    assert woq.device_status(clear=True) == _lib.WOQ_OK

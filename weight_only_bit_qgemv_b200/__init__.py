@@ -46,6 +46,8 @@ __all__ = [
     "qgemm",
     "qgemm_workspace_bytes",
     "qgemm_bf16_noalloc",
+    "attn_prompt",
+    "attn_prompt_workspace",
     "KV4Cache",
     "kv4_append",
     "kv4_gather",
@@ -294,28 +296,86 @@ def qgemm_bf16_noalloc(X: torch.Tensor, w: PackedWeight, out: torch.Tensor | Non
 _DTYPES = {torch.float32: _lib.WOQ_F32, torch.float16: _lib.WOQ_F16, torch.bfloat16: _lib.WOQ_BF16}
 
 
+def _device_of(t: torch.Tensor, what: str) -> int:
+    """The current CUDA device, which has to be the tensor's."""
+    d = t.get_device()
+    if d < 0 or d != torch.cuda.current_device():
+        raise ValueError(f"{what} must be on the current CUDA device")
+    return d
+
+
 def _rows(t: torch.Tensor, what: str, device: int) -> _lib.WoqRows:
     """The [rows, heads, dim] tensor ``t`` as the C ABI takes it; dim contiguous."""
-    if t.dtype not in _DTYPES or t.dim() != 3 or t.stride(2) != 1 or t.get_device() != device:
+    dtype = _DTYPES.get(t.dtype)
+    if dtype is None or t.dim() != 3 or t.get_device() != device or t.stride(2) != 1:
         raise ValueError(
             f"{what} must be a float32, float16 or bfloat16 tensor [rows, heads, dim] on the current CUDA device, "
             "contiguous along dim"
         )
-    row, head, _ = t.stride()
     n, heads, dim = t.shape
     # the stride of a dimension of one element says nothing
-    head = head if heads > 1 else dim
-    return _lib.WoqRows(t.data_ptr(), _DTYPES[t.dtype], heads, row if n > 1 else heads * head, head)
+    head = t.stride(1) if heads > 1 else dim
+    return _lib.WoqRows(t.data_ptr(), dtype, heads, t.stride(0) if n > 1 else heads * head, head)
 
 
 def _ints(t: torch.Tensor, what: str, dims: int, device: int) -> int:
-    if t.dtype != torch.int32 or t.dim() != dims or not t.is_contiguous() or t.get_device() != device:
+    if t.dtype != torch.int32 or t.dim() != dims or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dims}-D int32 tensor on the current CUDA device")
     return t.data_ptr()
 
 
-def _device() -> int:
-    return torch.cuda.current_device() if torch.cuda.is_available() else -2
+def _space(workspace: torch.Tensor | None, device: int) -> tuple[int | None, int]:
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def _raw_stream(stream, device: int) -> int:
+    # the handle alone: a torch.cuda.Stream object for it costs as much as the rest of a call
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
+def attn_prompt_workspace(q: torch.Tensor, k: torch.Tensor, batch: int) -> torch.Tensor | None:
+    """A workspace for attn_prompt calls with rows shaped like ``q`` and ``k`` in ``batch`` sequences; None if
+    they need none (16-bit types)."""
+    if q.dtype not in _DTYPES or q.dim() != 3 or k.dim() != 3:
+        raise ValueError("q and k must be float32, float16 or bfloat16 tensors [tokens, heads, dim]")
+    need = _lib.lib().attn_prompt_workspace_bytes(q.shape[0], batch, q.shape[1], k.shape[1], q.shape[2],
+                                                  _DTYPES[q.dtype])
+    return torch.empty(int(need), dtype=torch.uint8, device=q.device) if need else None
+
+
+def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, scale: float | None = None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Causal attention of packed sequences (C ABI ``attn_prompt``): q [tokens, heads, dim] over k, v
+    [tokens, kv_heads, dim], sequence b in rows cu[b] .. cu[b + 1] - 1. ``scale`` defaults to dim^-1/2;
+    without ``workspace`` (attn_prompt_workspace) one is made for the call. Rows of no sequence are left as they
+    are in ``out`` (zeros in a new one)."""
+    d = _device_of(q, "q")
+    qr, kr, vr = _rows(q, "q", d), _rows(k, "k", d), _rows(v, "v", d)
+    cp = _ints(cu, "cu", 1, d)
+    tokens, heads, dim = q.shape
+    if k.shape != v.shape or k.shape[0] != tokens or k.shape[2] != dim or not q.dtype == k.dtype == v.dtype:
+        raise ValueError("q, k and v must have one type, as many rows and one dim, k and v one shape")
+    if out is None:
+        with torch.cuda.stream(stream):
+            out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
+    orow = _rows(out, "out", d)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError("out must have q's shape and type")
+    batch = cu.numel() - 1
+    if workspace is None:
+        # made and given back on the stream that uses it
+        with torch.cuda.stream(stream):
+            workspace = attn_prompt_workspace(q, k, batch)
+    ws, nbytes = _space(workspace, d)
+    rc = _lib.lib().attn_prompt(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), tokens, cp, batch, dim,
+                                dim**-0.5 if scale is None else scale, ctypes.byref(orow), ws, nbytes,
+                                _raw_stream(stream, d))
+    _lib.check(rc, "attn_prompt")
+    return out
 
 
 @dataclass(frozen=True)
@@ -364,15 +424,9 @@ class KV4Cache:
     def nbytes(self) -> int:
         return self.codes.numel() + 2 * self.scales.numel()
 
-    def _on(self, device: int):
-        if self.codes.get_device() != device:
-            raise ValueError("the cache must be on the current CUDA device")
-        return ctypes.byref(self._desc)
-
-
 def _step_args(cache, k, v, cu, table, start, what):
-    d = _device()
-    c = cache._on(d)
+    d = _device_of(cache.codes, "the cache")
+    c = ctypes.byref(cache._desc)
     kr, vr = _rows(k, f"{what}: k", d), _rows(v, f"{what}: v", d)
     if k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.dim):
         raise ValueError(f"{what}: k and v must be [tokens, {cache.kv_heads}, {cache.dim}]")
@@ -382,7 +436,7 @@ def _step_args(cache, k, v, cu, table, start, what):
     sp = None if start is None else _ints(start, "start", 1, d)
     if cu.numel() != batch + 1 or (start is not None and start.numel() != batch):
         raise ValueError(f"{what}: cu has batch + 1 entries, start and table batch")
-    return c, kr, vr, cp, sp, batch, tp, width
+    return d, c, kr, vr, cp, sp, batch, tp, width
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tensor, table: torch.Tensor,
@@ -390,9 +444,9 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tens
     """Quantise packed rows of keys and values [tokens, kv_heads, dim] into the cache's pages
     (C ABI ``kv4_append``). Rows cu[b] .. cu[b + 1] - 1 become tokens start[b], start[b] + 1, ... of
     sequence b, whose pages are table[b]; ``start`` None: each sequence is new."""
-    c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k, v, cu, table, start, "kv4_append")
+    d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k, v, cu, table, start, "kv4_append")
     rc = _lib.lib().kv4_append(c, ctypes.byref(kr), ctypes.byref(vr), k.shape[0], cp, sp, batch, tp, width,
-                               _stream(stream))
+                               _raw_stream(stream, d))
     _lib.check(rc, "kv4_append")
 
 
@@ -406,10 +460,11 @@ def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: to
         raise ValueError("kv4_gather takes k_out and v_out, or tokens")
     if k_out is None:
         shape = (tokens, cache.kv_heads, cache.dim)
-        k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.codes.device) for _ in "kv")
-    c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k_out, v_out, cu, table, start, "kv4_gather")
+        with torch.cuda.stream(stream):
+            k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.codes.device) for _ in "kv")
+    d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k_out, v_out, cu, table, start, "kv4_gather")
     rc = _lib.lib().kv4_gather(c, cp, sp, batch, tp, width, k_out.shape[0], ctypes.byref(kr), ctypes.byref(vr),
-                               _stream(stream))
+                               _raw_stream(stream, d))
     _lib.check(rc, "kv4_gather")
     return k_out, v_out
 
@@ -426,8 +481,8 @@ def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.
     """One-token attention [batch, heads, dim] over the first lens[b] cached tokens of each sequence
     (C ABI ``kv4_attn``). ``scale`` defaults to dim^-1/2; without ``workspace`` one is made for the
     call."""
-    d = _device()
-    c = cache._on(d)
+    d = _device_of(cache.codes, "the cache")
+    c = ctypes.byref(cache._desc)
     qr = _rows(q, "q", d)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
@@ -440,11 +495,9 @@ def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.
         # made, zeroed and given back on the stream that uses it
         with torch.cuda.stream(stream):
             workspace = kv4_attn_workspace(cache, q)
-    elif workspace.get_device() != d or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    ws, nbytes = _space(workspace, d)
     rc = _lib.lib().kv4_attn(ctypes.byref(qr), c, lp, batch, tp, width, cache.dim**-0.5 if scale is None else scale,
-                             ctypes.byref(orow), _ptr(workspace), workspace.numel() * workspace.element_size(),
-                             _stream(stream))
+                             ctypes.byref(orow), ws, nbytes, _raw_stream(stream, d))
     _lib.check(rc, "kv4_attn")
     return out
 

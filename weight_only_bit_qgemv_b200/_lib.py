@@ -48,6 +48,8 @@ EXPORTS = (
     "qgemm_workspace_bytes",
     "qgemm",
     "qgemm_bf16_noalloc",
+    "attn_prompt_workspace_bytes",
+    "attn_prompt",
     "kv4_append",
     "kv4_gather",
     "kv4_attn_workspace_bytes",
@@ -147,6 +149,10 @@ def lib() -> ctypes.CDLL:
     L.qgemm_bf16_noalloc.argtypes = [vp, c_i64, wp, vp, vp]
     L.qgemm_bf16_noalloc.restype = ctypes.c_int
     rp, cp = ctypes.POINTER(WoqRows), ctypes.POINTER(WoqKv4)
+    L.attn_prompt_workspace_bytes.argtypes = [c_i64, c_i32, c_i32, c_i32, c_i32, c_i32]
+    L.attn_prompt_workspace_bytes.restype = ctypes.c_size_t
+    L.attn_prompt.argtypes = [rp, rp, rp, c_i64, vp, c_i32, c_i32, ctypes.c_float, rp, vp, ctypes.c_size_t, vp]
+    L.attn_prompt.restype = ctypes.c_int
     L.kv4_append.argtypes = [cp, rp, rp, c_i64, vp, vp, c_i32, vp, c_i64, vp]
     L.kv4_append.restype = ctypes.c_int
     L.kv4_gather.argtypes = [cp, vp, vp, c_i32, vp, c_i64, c_i64, rp, rp, vp]

@@ -14,7 +14,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libwoq.so")
 
 CU_SOURCES = ["api.cu", "qgemv.cu", "qgemv_tc.cu", "qgemv_i8tc.cu", "qgemv_chain.cu", "qgemm_tc.cu", "qgemm_noalloc.cu",
-              "kv4.cu", "kv4_attn.cu", "api_attn.cu"]
+              "kv4.cu", "kv4_attn.cu", "attn_prompt.cu", "api_attn.cu"]
 CXX_SOURCES = ["qpack.cpp"]
 HEADERS = ["ptx.cuh", "woq_internal.h", "gemv_math.cuh", "kv4.cuh"]
 

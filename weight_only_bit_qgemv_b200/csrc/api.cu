@@ -272,7 +272,7 @@ int qgemm(const float *X, int64_t m, const woq_weight *w, float *Y, int32_t path
 
 int woq_device_status(int clear) {
   if (cudaDeviceSynchronize() != cudaSuccess) return WOQ_ECUDA;
-  unsigned v = 0, g = 0, t = 0, i = 0, c = 0, a = 0;
+  unsigned v = 0, g = 0, t = 0, i = 0, c = 0, a = 0, p = 0;
   int rc = woq::read_wait_timeout_flag(clear, &v);
   if (rc != WOQ_OK) return rc;
   rc = woq::read_gemv_timeout_flag(clear, &g);
@@ -285,7 +285,9 @@ int woq_device_status(int clear) {
   if (rc != WOQ_OK) return rc;
   rc = woq::read_kv4_timeout_flag(clear, &a);
   if (rc != WOQ_OK) return rc;
-  return (v || g || t || i || c || a) ? WOQ_ETIMEOUT : WOQ_OK;
+  rc = woq::read_prompt_timeout_flag(clear, &p);
+  if (rc != WOQ_OK) return rc;
+  return (v || g || t || i || c || a || p) ? WOQ_ETIMEOUT : WOQ_OK;
 }
 
 void woq_debug_set_wait_limit(long long cycles) { woq::set_wait_limit_cycles(cycles); }

@@ -9,7 +9,7 @@
 namespace woq {
 namespace {
 
-constexpr int kMaxHeads = 1 << 16;
+constexpr int kMaxSequences = 1 << 20;
 constexpr int kMaxGroup = 64;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -142,6 +142,47 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
   if (rc != WOQ_OK) return rc;
   return woq::launch_kv4_attn(*q, *cache, lens, batch, table, width, scale, *o, workspace,
                               static_cast<cudaStream_t>(stream), dev);
+}
+
+static bool prompt_heads(int32_t q_heads, int32_t kv_heads) {
+  return kv_heads >= 1 && kv_heads <= 1024 && q_heads >= 1 && q_heads <= 32768 && q_heads % kv_heads == 0;
+}
+
+size_t attn_prompt_workspace_bytes(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                                   int32_t dtype) {
+  if (tokens < 0 || tokens > INT32_MAX || batch < 1 || batch > woq::kMaxSequences) return 0;
+  if (!prompt_heads(q_heads, kv_heads) || (dim != 64 && dim != 128)) return 0;
+  return woq::attn_prompt_workspace(tokens, batch, q_heads, kv_heads, dim, dtype);
+}
+
+int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
+                int32_t batch, int32_t dim, float scale, const woq_rows *o, void *workspace,
+                size_t workspace_bytes, void *stream) {
+  if (!q || !k || !v || !o || !cu || tokens < 0 || batch < 1 || batch > woq::kMaxSequences) return WOQ_EINVAL;
+  if (dim != 64 && dim != 128) return WOQ_ESHAPE;
+  if (!prompt_heads(q->heads, k->heads)) return WOQ_EINVAL;
+  const woq_rows *all[4] = {q, k, v, o};
+  for (int i = 0; i < 4; ++i) {
+    const int rc = woq::check_rows(all[i], i == 0 || i == 3 ? q->heads : k->heads, dim);
+    if (rc != WOQ_OK) return rc;
+    if (all[i]->dtype != q->dtype) return WOQ_EINVAL;
+  }
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
+  if (!woq::aligned(cu, 4)) return WOQ_EALIGN;
+  if (tokens > INT32_MAX || (tokens / 256 + batch) * q->heads > INT32_MAX) return WOQ_ESHAPE;
+  if (tokens > 0)
+    for (int i = 0; i < 3; ++i)
+      if (woq::overlap(*all[i], *o, tokens, dim)) return WOQ_EINVAL;
+  const size_t need = woq::attn_prompt_workspace(tokens, batch, q->heads, k->heads, dim, q->dtype);
+  if (need > 0 && tokens > 0) {
+    if (!workspace || workspace_bytes < need) return WOQ_EWORKSPACE;
+    if (!woq::aligned(workspace, 256)) return WOQ_EALIGN;
+  }
+  DevInfo dev;
+  const int rc = woq::current_device(&dev);
+  if (rc != WOQ_OK || tokens == 0) return rc;
+  return woq::launch_attn_prompt(*q, *k, *v, tokens, cu, batch, dim, scale, *o, workspace,
+                                 static_cast<cudaStream_t>(stream), dev);
 }
 
 }  // extern "C"

@@ -1,0 +1,878 @@
+// attn_prompt: causal attention over whole prompts, packed one after another.
+//   s_ij = scale q_i . k_j,  o_i = sum_{j <= i} softmax_j(s_ij) v_j
+//
+// Bound: 16-bit rows, the exponentials and what surrounds them (2 * dim * 2 flop of tensor work to an
+// exponential: at dim 128 the tensor cores want 16,384 of them every 512 cycles of an SM, whose
+// special-function units make 16 a cycle); float32 rows, the tensor cores (three products for one).
+//
+// One block an SM takes 256 query rows of one head as two tiles of 128 and walks the keys in tiles of
+// BK up to the diagonal. Two warpgroups have a query tile each, a row a thread: they read the scores
+// from tensor memory, keep the row's running maximum and sum, write the weights back to
+// tensor memory (over the scores) and hold the output in registers. While one has its
+// exponentials, the tensor cores work for the other. The third group's warps: 0 copies (TMA), 1 issues
+// the matrix instructions, 2 and 3 look at the values of the tiles on the diagonal.
+//
+// The output is summed in registers, not in tensor memory: each tile's product starts from zero, so that
+// sums inside the tensor cores, which cut off instead of rounding, run over BK keys at most, and so that a new
+// maximum costs nothing but the factor of a multiply-add.
+//
+// float32 rows: a kernel before writes each tile of 64 rows as two binary16 planes, high part and rest, times the
+// power of two that brings its largest finite value into [2^13, 2^14) (query rows each by itself): 22 bits of
+// every value within 2^17 of its tile's largest. Scores are three products (high x high and the two mixed
+// ones, small ones first), the weights are split the same way, times 2^13.
+//
+// Masked weights are exact zeros, but zero times a value that is not finite is NaN. The tiles on the diagonal hold
+// every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory, and
+// added after the last tile to the rows that do see it.
+#include <algorithm>
+#include <mutex>
+
+#include "kv4.cuh"
+#include "ptx.cuh"
+#include "woq_internal.h"
+
+namespace woq {
+
+__device__ unsigned int g_prompt_timeout_flag = 0;
+
+namespace {
+
+constexpr int kRows = 128;               // query rows of a warpgroup: the lanes of tensor memory
+constexpr int kBlockRows = 2 * kRows;
+constexpr int kSplitRows = 64;           // rows of a float32 tile with one power of two
+constexpr int kThreads = 384;
+constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kHelperRegs = 56;
+static_assert(256 * kConsumerRegs + 128 * kHelperRegs <= kThreads * kLaunchRegs, "register split");
+constexpr uint32_t kTmemCols = 512;
+constexpr long long kWaitLimit = 1LL << 32;   // cycles (~2 s)
+constexpr long long kDrainLimit = 1LL << 31;
+
+enum { kBf16 = 0, kF16 = 1, kSplit = 2 };
+
+template <int D, int MODE>
+struct Cfg {
+  static constexpr int Parts = MODE == kSplit ? 2 : 1;       // planes of an operand
+  static constexpr int BK = MODE == kSplit ? 64 : 128;       // keys of a tile
+  static constexpr int Subs = D / 64;                        // 128-byte columns of a tile
+  static constexpr int QBytes = Parts * kRows * D * 2;
+  static constexpr int KvBytes = Parts * BK * D * 2;
+  static constexpr int Room = 227 * 1024 - 2048 - 2 * QBytes;
+  static constexpr int Stages = Room / KvBytes > 6 ? 6 : Room / KvBytes;
+  static_assert(Stages >= 3, "keys and values of two tiles are in flight at once");
+  static constexpr int Smem = 2 * QBytes + Stages * KvBytes + 2048;
+};
+
+struct Maps {
+  CUtensorMap q[2], k[2], v[2];  // [plane]
+};
+
+struct Args {
+  const int32_t *cu;
+  int64_t tokens;
+  int batch, q_heads, group;
+  float scale;  // times log2(e)
+  woq_rows o, v;
+  // float32 rows: powers of two by row (queries) and by tile of kSplitRows (keys, values)
+  const float *q_pow, *k_pow, *v_pow;
+  int64_t tiles;  // entries of a head in k_pow and v_pow
+  long long wait_limit, stuck_wait;
+};
+
+struct Shared {
+  uint64_t q_full[2];
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], p_full[2], t_full[2], t_empty[2];
+  uint64_t look[kBlockRows / 64];    // the copy of a diagonal tile's values is under way
+  uint64_t looked[kBlockRows / 64];  // they are there, and finite
+  uint64_t looked_all;
+  uint64_t drain, never;
+  uint32_t tmem;
+  int abort;
+  int nonfinite;
+  int b, r0, start, len, tile0;  // the block's rows
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void record_timeout(volatile int *abort) {
+  *abort = 1;
+  atomicOr(&g_prompt_timeout_flag, 1u);
+}
+
+// Tile `target` of all sequences' tiles of `rows` rows: its sequence's rows, its place there, and how
+// many tiles of kSplitRows the sequences before have. One warp. False if there are fewer tiles.
+struct Place {
+  int start, len, tile, tiles, split0;
+};
+__device__ bool find_tile(const int32_t *cu, int batch, int64_t tokens, int64_t target, int rows, Place &p) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  int split = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const int b = b0 + lane;
+    int64_t s = 0, e = 0;
+    if (b < batch) {
+      s = cu[b];
+      e = cu[b + 1];
+      s = s < 0 ? 0 : s > tokens ? tokens : s;
+      e = e < s ? s : e > tokens ? tokens : e;
+    }
+    const int len = static_cast<int>(e - s);
+    const int n = (len + rows - 1) / rows, ns = (len + kSplitRows - 1) / kSplitRows;
+    int sum = n, sums = ns;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, i), y = __shfl_up_sync(0xffffffffu, sums, i);
+      if (lane >= i) {
+        sum += x;
+        sums += y;
+      }
+    }
+    const unsigned has = __ballot_sync(0xffffffffu, before + sum > target);
+    if (has) {
+      const int l = __ffs(has) - 1;
+      p.start = __shfl_sync(0xffffffffu, static_cast<int>(s), l);
+      p.len = __shfl_sync(0xffffffffu, len, l);
+      p.tiles = __shfl_sync(0xffffffffu, n, l);
+      p.tile = static_cast<int>(target - before - (__shfl_sync(0xffffffffu, sum, l) - p.tiles));
+      p.split0 = split + __shfl_sync(0xffffffffu, sums - ns, l);
+      return true;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+    split += __shfl_sync(0xffffffffu, sums, 31);
+  }
+  return false;
+}
+
+// Shared-memory matrix descriptors, 128-byte swizzle. Rows along the summed dimension's other side
+// (queries, keys of the first product): 8-row groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Values: rows are the summed dimension, 8 of them 1024 bytes apart, and 64-element columns
+// `sub_bytes` apart.
+__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr, uint32_t sub_bytes) {
+  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>(sub_bytes >> 4) << 16) |
+         (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: FP32 result, M = 128, N = n; `cols`: B's rows are the summed dimension.
+__host__ __device__ constexpr uint32_t idesc_for(int n, bool bf16, bool cols) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (cols ? 1u << 16 : 0u) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+template <int MODE>
+__device__ __forceinline__ uint32_t pack(float a, float b) {
+  return pack2(a, b, MODE == kBf16 ? WOQ_BF16 : WOQ_F16);
+}
+
+template <int D, int MODE>
+__global__ void __launch_bounds__(kThreads, 1)
+    attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
+  using C = Cfg<D, MODE>;
+  constexpr int BK = C::BK, ST = C::Stages;
+  constexpr uint32_t kScores = 0, kTile = 2 * BK;  // tensor memory columns: scores, products with the values
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *smem_kv = smem + 2 * C::QBytes;
+  Shared &sh = *reinterpret_cast<Shared *>(smem_kv + ST * C::KvBytes);
+  volatile int *abort = &sh.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  ptx::pdl_wait();
+  const int head = static_cast<int>(blockIdx.x % a.q_heads);
+  if (warp == 0) {
+    Place p{};
+    const bool found = find_tile(a.cu, a.batch, a.tokens, blockIdx.x / a.q_heads, kBlockRows, p);
+    if (lane == 0) {
+      sh.len = found ? p.len : 0;
+      sh.start = p.start;
+      sh.r0 = found ? (p.tiles - 1 - p.tile) * kBlockRows : 0;  // a sequence's longest rows first
+      sh.tile0 = p.split0;
+      sh.abort = 0;
+      sh.nonfinite = 0;
+    }
+  }
+  if (warp == 1 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh.q_full[i], 1);
+      ptx::mbar_init(&sh.s_full[i], 1);
+      ptx::mbar_init(&sh.p_full[i], 4);
+      ptx::mbar_init(&sh.t_full[i], 1);
+      ptx::mbar_init(&sh.t_empty[i], 4);
+    }
+    for (int i = 0; i < ST; ++i) {
+      ptx::mbar_init(&sh.kv_full[i], 1);
+      ptx::mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i < kBlockRows / 64; ++i) {
+      ptx::mbar_init(&sh.look[i], 1);
+      ptx::mbar_init(&sh.looked[i], 2);
+    }
+    ptx::mbar_init(&sh.looked_all, 2);
+    ptx::mbar_init(&sh.drain, 1);
+    ptx::mbar_init(&sh.never, 1);
+    ptx::fence_mbar_init();
+  }
+  __syncthreads();
+  const int len = sh.len, r0 = sh.r0, start = sh.start;
+  if (len == 0) {  // fewer tiles than blocks
+    ptx::pdl_launch_dependents();
+    return;
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&sh.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+
+  // Key tiles of the two query tiles: up to the diagonal, and not behind the last row.
+  auto tiles_of = [&](int t) {
+    const int first = r0 + t * kRows;
+    const int rows = min(len, first + kRows);
+    return first < len ? (rows + BK - 1) / BK : 0;
+  };
+  const int n0 = tiles_of(0), n1 = tiles_of(1);
+  const int nt = max(n0, n1);
+  const int diag = r0 / BK;  // the first tile with masked pairs
+  const int kv_head = head / a.group;
+
+  bool mma_issued = false;
+  int issued = 0;  // copies' slots filled so far
+
+  if (warp >= 8) {
+    ptx::regs_dec<kHelperRegs>();
+    if (warp == 8) {
+      // ---- copies: q 0, k 0, q 1, v 0, k 1, v 1, ... ----
+      if (lane == 0) {
+        for (int p = 0; p < C::Parts; ++p) {
+          ptx::prefetch_tmap(&maps.q[p]);
+          ptx::prefetch_tmap(&maps.k[p]);
+          ptx::prefetch_tmap(&maps.v[p]);
+        }
+        auto query = [&](int t) {
+          ptx::mbar_arrive_expect_tx(&sh.q_full[t], C::QBytes);
+          for (int p = 0; p < C::Parts; ++p)
+            for (int c = 0; c < C::Subs; ++c)
+              ptx::tma_load_3d(smem + t * C::QBytes + (p * C::Subs + c) * kRows * 128, &maps.q[p], &sh.q_full[t],
+                               64 * c, head, start + r0 + t * kRows);
+        };
+        auto kv = [&](const CUtensorMap *m, int tile) {
+          const int slot = issued % ST;
+          if (!ptx::mbar_wait_bounded(&sh.kv_empty[slot], ((issued / ST) & 1) ^ 1, a.wait_limit, abort)) {
+            record_timeout(abort);
+            return false;
+          }
+          ptx::mbar_arrive_expect_tx(&sh.kv_full[slot], C::KvBytes);
+          for (int p = 0; p < C::Parts; ++p)
+            for (int c = 0; c < C::Subs; ++c)
+              ptx::tma_load_3d(smem_kv + slot * C::KvBytes + (p * C::Subs + c) * BK * 128, &m[p],
+                               &sh.kv_full[slot], 64 * c, kv_head, start + tile * BK);
+          ++issued;
+          return true;
+        };
+        query(0);
+        bool ok = kv(maps.k, 0);
+        if (n1 > 0) query(1);
+        for (int j = 0; j < nt && ok; ++j) {
+          ok = kv(maps.v, j);
+          if (ok && j >= diag) ptx::mbar_arrive(&sh.look[j - diag]);
+          ok = ok && (j + 1 == nt || kv(maps.k, j + 1));
+        }
+      }
+    } else if (warp == 9) {
+      // ---- matrix instructions ----
+      if (lane == 0) {
+        constexpr uint32_t kIdescS = idesc_for(BK, MODE == kBf16, false), kIdescT = idesc_for(D, MODE == kBf16, true);
+        constexpr int kPlaneQ = kRows * D * 2, kPlaneK = BK * D * 2;
+        bool ok = true;
+        if (a.stuck_wait > 0 && !ptx::mbar_wait_bounded(&sh.never, 0, a.stuck_wait, abort)) {  // test hook
+          record_timeout(abort);
+          ok = false;
+        }
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+          if (ok && !ptx::mbar_wait_bounded(bar, parity, a.wait_limit, abort)) {
+            record_timeout(abort);
+            ok = false;
+          }
+          return ok;
+        };
+        const uint32_t q_addr = ptx::smem_u32(smem), kv_addr = ptx::smem_u32(smem_kv);
+        auto scores = [&](int t, int slot) {
+          const uint32_t d = tmem + kScores + t * BK;
+          const uint32_t q = q_addr + t * C::QBytes, k = kv_addr + slot * C::KvBytes;
+          uint32_t acc = 0;
+          auto product = [&](int pq, int pk) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk & 3) * 32;
+              ptx::tc_mma_f16(d, desc_rows(q + pq * kPlaneQ + (kk >> 2) * kRows * 128 + off),
+                              desc_rows(k + pk * kPlaneK + (kk >> 2) * BK * 128 + off), kIdescS, acc);
+              acc = 1;
+            }
+          };
+          if constexpr (MODE == kSplit) {
+            product(1, 0);
+            product(0, 1);
+          }
+          product(0, 0);
+          mma_issued = true;
+          ptx::tc_commit(&sh.s_full[t]);
+        };
+        auto values = [&](int t, int slot) {
+          const uint32_t d = tmem + kTile + t * D, p = tmem + kScores + t * BK;
+          const uint32_t v = kv_addr + slot * C::KvBytes;
+          uint32_t acc = 0;
+          auto product = [&](int pp, int pv) {
+#pragma unroll
+            for (int kk = 0; kk < BK / 16; ++kk) {
+              ptx::tc_mma_f16_ts(d, p + pp * (BK / 2) + kk * 8, desc_cols(v + pv * kPlaneK + kk * 2048, BK * 128),
+                                 kIdescT, acc);
+              acc = 1;
+            }
+          };
+          if constexpr (MODE == kSplit) {
+            product(1, 0);
+            product(0, 1);
+          }
+          product(0, 0);
+          ptx::tc_commit(&sh.t_full[t]);
+        };
+        // Slot number i of the ring holds k 0, v 0, k 1, v 1, ... in this order.
+        auto full = [&](int i) { return wait(&sh.kv_full[i % ST], (i / ST) & 1); };
+        if (wait(&sh.q_full[0], 0) && full(0)) {
+          scores(0, 0);
+          if (n1 > 0 && wait(&sh.q_full[1], 0)) scores(1, 0);
+          ptx::tc_commit(&sh.kv_empty[0]);
+        }
+        for (int j = 0; j < nt && ok; ++j) {
+          const int vi = 2 * j + 1, ki = 2 * j + 2;
+          if (!full(vi) || (j >= diag && !wait(&sh.looked[j - diag], 0))) break;
+          bool k_there = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            const int n = t ? n1 : n0;
+            if (j >= n) continue;
+            if (!wait(&sh.p_full[t], j & 1) || !wait(&sh.t_empty[t], (j & 1) ^ 1)) break;
+            ptx::tc_fence_after();
+            values(t, vi % ST);
+            if (j + 1 < n) {
+              if (!k_there && !full(ki)) break;
+              k_there = true;
+              scores(t, ki % ST);
+            }
+          }
+          if (!ok) break;
+          ptx::tc_commit(&sh.kv_empty[vi % ST]);
+          if (k_there) ptx::tc_commit(&sh.kv_empty[ki % ST]);
+        }
+        ptx::tc_commit(&sh.drain);
+      }
+    } else {
+      // ---- values on the diagonal: what is not finite becomes 0 ----
+      constexpr uint32_t kExp = MODE == kBf16 ? 0x7f807f80u : 0x7c007c00u;
+      constexpr uint32_t kOne = MODE == kBf16 ? 0x00800080u : 0x04000400u;
+      const int tid = threadIdx.x - 10 * 32;
+      bool ok = true;
+      for (int j = diag; j < nt && ok; ++j) {
+        const int i = 2 * j + 1;
+        // The slot's phase is this tile's from the copy's start until the tile has been looked at: only
+        // then does its parity mean this tile.
+        ok = __all_sync(0xffffffffu,
+                        ptx::mbar_wait_bounded(&sh.look[j - diag], 0, a.wait_limit, abort) &&
+                            ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, a.wait_limit, abort));
+        if (!ok) {
+          record_timeout(abort);
+          break;
+        }
+        // The high plane; the other is finite in the sequence's rows, and unknown behind them.
+        uint4 *tile = reinterpret_cast<uint4 *>(smem_kv + (i % ST) * C::KvBytes);
+        const int planes = (j + 1) * BK > len ? C::Parts : 1;
+        bool mine = false, wrote = false;
+        for (int c = tid; c < planes * BK * D / 8; c += 64) {
+          uint4 x = tile[c];
+          uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+          uint32_t bad = 0;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) bad |= (w[k] & kExp) + kOne;
+          if (bad & 0x80008000u) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t b = ((w[k] & kExp) + kOne) & 0x80008000u;
+              if (b & 0x8000u) w[k] &= 0xffff0000u;
+              if (b & 0x80000000u) w[k] &= 0xffffu;
+            }
+            tile[c] = x;
+            wrote = true;
+            mine |= j * BK + c / 8 % BK < len;  // not of the rows behind the sequence
+          }
+        }
+        if (mine) sh.nonfinite = 1;
+        if (wrote) ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.looked[j - diag]);
+      }
+      if (lane == 0) ptx::mbar_arrive(&sh.looked_all);
+    }
+  } else {
+    // ---- a query tile: one row a thread ----
+    ptx::regs_inc<kConsumerRegs>();
+    const int t = warp >> 2;
+    const int row = r0 + t * kRows + (threadIdx.x & 127);
+    const int n = t ? n1 : n0;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + kScores + t * BK, t_addr = tmem + lanes + kTile + t * D;
+    float2 o[D / 2];
+#pragma unroll
+    for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0, 0);
+    float m = -INFINITY, l = 0, alpha = 0, v_pow = 1;
+    float scale = a.scale;
+    const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
+    if constexpr (MODE == kSplit) {
+      if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
+    }
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t parity) {
+      if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, a.wait_limit, abort))) {
+        record_timeout(abort);
+        ok = false;
+      }
+      return ok;
+    };
+    // o = o alpha + the last tile's product
+    auto accumulate = [&](int j) {
+      if (!wait(&sh.t_full[t], j & 1)) return;
+      ptx::tc_fence_after();
+      const float2 al = make_float2(alpha, alpha), vp = make_float2(v_pow, v_pow);
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        ptx::tmem_ld_32x32b_x32(t_addr + 32 * c, x);
+        ptx::tmem_ld_wait(x);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float2 y = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
+          float2 &z = o[16 * c + i];
+          z = MODE == kSplit ? __ffma2_rn(z, al, __fmul2_rn(y, vp)) : __ffma2_rn(z, al, y);
+        }
+      }
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.t_empty[t]);
+    };
+    for (int j = 0; j < n && ok; ++j) {
+      float k_pow = 1, v_next = 1;
+      if constexpr (MODE == kSplit) {
+        const int64_t at = pow0 + min(static_cast<int64_t>(sh.tile0) + j, a.tiles - 1);
+        k_pow = __ldg(a.k_pow + at);
+        v_next = __ldg(a.v_pow + at);
+      }
+      if (j > 0) accumulate(j - 1);
+      if (!ok || !wait(&sh.s_full[t], j & 1)) break;
+      v_pow = v_next;
+      ptx::tc_fence_after();
+      const float c = scale * k_pow;
+      const int lim = row - j * BK;  // the last column that this row sees
+      const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
+      float mx = -INFINITY;
+      auto load = [&](int ch, uint32_t (&x)[32]) {
+        ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x);
+        ptx::tmem_ld_wait(x);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (32 * ch + i > lim) x[i] = 0xff800000u;
+        }
+      };
+      auto top = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
+      };
+      // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
+      float2 sum = make_float2(0, 0);
+      const float2 cc = make_float2(c, c);
+      float2 ref;
+      auto settle = [&] {
+        // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
+        const float m2 = fmaxf(m, fmaxf(mx * c, -3.402823466e38f));
+        const float r = (MODE == kSplit ? 13.0f : 0.0f) - m2;
+        ref = make_float2(r, r);
+        alpha = ex2(m - m2);
+        l *= alpha;
+        m = m2;
+      };
+      auto weights = [&](int ch, uint32_t (&x)[32]) {
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
+          y = make_float2(ex2(y.x), ex2(y.y));
+          sum = __fadd2_rn(sum, y);
+          hi[i] = pack<MODE>(y.x, y.y);
+          if constexpr (MODE == kSplit) {
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+            lo[i] = pack<MODE>(y.x - h.x, y.y - h.y);
+          }
+        }
+        ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
+        if constexpr (MODE == kSplit) ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+      };
+      if constexpr (BK == 64) {
+        uint32_t x0[32], x1[32];  // both chunks are read before the weights overwrite them
+        load(0, x0);
+        load(1, x1);
+        top(x0);
+        top(x1);
+        settle();
+        weights(0, x0);
+        weights(1, x1);
+      } else {
+        uint32_t x[32];
+#pragma unroll
+        for (int ch = 0; ch < BK / 32; ++ch) {
+          load(ch, x);
+          top(x);
+        }
+        settle();
+#pragma unroll
+        for (int ch = 0; ch < BK / 32; ++ch) {  // weights go to columns that have been read
+          load(ch, x);
+          weights(ch, x);
+        }
+      }
+      l += sum.x + sum.y;
+      ptx::tmem_st_wait();
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+    }
+    if (ok && n > 0) accumulate(n - 1);
+    if (ok && n > 0) wait(&sh.looked_all, 0);
+    if (ok && row < len) {
+      const float inv = 1.0f / l;
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
+      if (sh.nonfinite) {
+        // Values on the diagonal that are not finite, in the rows that see them.
+        for (int j = diag * BK; j <= row; ++j) {
+          const int64_t at = (start + j) * a.v.row_stride + kv_head * a.v.head_stride;
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i) {
+            const float4 x = load4(a.v.data, at + 4 * i, a.v.dtype);
+            if (!isfinite(x.x)) o[2 * i].x += x.x;
+            if (!isfinite(x.y)) o[2 * i].y += x.y;
+            if (!isfinite(x.z)) o[2 * i + 1].x += x.z;
+            if (!isfinite(x.w)) o[2 * i + 1].y += x.w;
+          }
+        }
+      }
+      const int64_t at = (start + row) * a.o.row_stride + head * a.o.head_stride;
+      if constexpr (MODE == kSplit) {
+        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o.data) + at);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
+      } else {
+        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.data) + at);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+          dst[i] = make_uint4(pack<MODE>(o[4 * i].x, o[4 * i].y), pack<MODE>(o[4 * i + 1].x, o[4 * i + 1].y),
+                              pack<MODE>(o[4 * i + 2].x, o[4 * i + 2].y), pack<MODE>(o[4 * i + 3].x, o[4 * i + 3].y));
+      }
+    }
+  }
+
+  // ---- teardown: what this block has in flight ends, then its tensor memory is freed ----
+  if (*abort) {
+    int no_abort = 0;
+    if (warp == 8 && lane == 0) {
+      ptx::mbar_wait_bounded(&sh.q_full[0], 0, kDrainLimit, &no_abort);
+      if (n1 > 0) ptx::mbar_wait_bounded(&sh.q_full[1], 0, kDrainLimit, &no_abort);
+      for (int i = max(0, issued - ST); i < issued; ++i)
+        ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, kDrainLimit, &no_abort);
+    }
+  }
+  if (warp == 9 && lane == 0 && mma_issued) {
+    int no_abort = 0;
+    ptx::mbar_wait_bounded(&sh.drain, 0, kDrainLimit, &no_abort);
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::pdl_launch_dependents();
+  if (warp == 9) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// ---- float32 rows -> two binary16 planes [heads][tokens][dim] and their powers of two -------------------
+
+struct SplitArgs {
+  woq_rows q, k, v;
+  const int32_t *cu;
+  int64_t tokens, tiles;
+  int batch;
+  __half *planes[3][2];
+  float *q_pow, *k_pow, *v_pow;
+};
+
+constexpr int kSplitThreads = 256;
+
+// x = hi + lo with 22 bits; what is not finite stays as it is, with nothing beside it.
+__device__ __forceinline__ void split4(float4 x, float up, uint2 &hi, uint2 &lo) {
+  const float *f = reinterpret_cast<const float *>(&x);
+  __half h[4], r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float y = f[i] * up;
+    h[i] = __float2half_rn(y);
+    r[i] = isfinite(f[i]) ? __float2half_rn(y - __half2float(h[i])) : __float2half_rn(0.0f);
+  }
+  auto two = [](__half a, __half b) {
+    const __half2 p = __halves2half2(a, b);
+    return *reinterpret_cast<const uint32_t *>(&p);
+  };
+  hi = make_uint2(two(h[0], h[1]), two(h[2], h[3]));
+  lo = make_uint2(two(r[0], r[1]), two(r[2], r[3]));
+}
+__device__ __forceinline__ float largest(float4 x) {  // of what is finite
+  auto f = [](float y) { return isfinite(y) ? fabsf(y) : 0.0f; };
+  return fmaxf(fmaxf(f(x.x), f(x.y)), fmaxf(f(x.z), f(x.w)));
+}
+// The power of two that a largest value in [2^13, 2^14) takes.
+__device__ __forceinline__ int exponent(float big) { return big > 0 ? max(min(ilogbf(big) - 13, 113), -113) : 0; }
+
+// Block (tile of 64 rows of a sequence, head of q, k or v): eight warps of eight rows, a lane four values of a row.
+template <int D>
+__global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a) {
+  constexpr int LANES = D / 4, ROWS = 8 * LANES / 32;  // rows that a lane has
+  __shared__ Place place;
+  __shared__ int found;
+  __shared__ float warp_big[8];
+  ptx::pdl_wait();
+  ptx::pdl_launch_dependents();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 0) {
+    Place p{};
+    const bool f = find_tile(a.cu, a.batch, a.tokens, blockIdx.x, kSplitRows, p);
+    if (lane == 0) {
+      place = p;
+      found = f;
+    }
+  }
+  __syncthreads();
+  if (!found) return;
+  const int hq = a.q.heads, hk = a.k.heads, y = blockIdx.y;
+  const int which = y < hq ? 0 : y < hq + hk ? 1 : 2;
+  const int head = which == 0 ? y : which == 1 ? y - hq : y - hq - hk;
+  const woq_rows &src = which == 0 ? a.q : which == 1 ? a.k : a.v;
+  const float *data = static_cast<const float *>(src.data);
+  const int col = 4 * (lane % LANES);
+  float4 x[ROWS];
+  int row[ROWS];
+  float big = 0;
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    row[i] = place.tile * kSplitRows + warp * 8 + i * (32 / LANES) + lane / LANES;
+    x[i] = make_float4(0, 0, 0, 0);
+    if (row[i] < place.len)
+      x[i] = *reinterpret_cast<const float4 *>(data + (place.start + row[i]) * src.row_stride +
+                                               head * src.head_stride + col);
+    big = fmaxf(big, largest(x[i]));
+  }
+  int ex = 0;
+  if (which != 0) {
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, i));
+    if (lane == 0) warp_big[warp] = big;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) big = fmaxf(big, warp_big[i]);
+    ex = exponent(big);
+    if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = ldexpf(1.0f, ex);
+  }
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    if (which == 0) {
+      float b = largest(x[i]);
+#pragma unroll
+      for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
+      ex = exponent(b);
+    }
+    if (row[i] >= place.len) continue;
+    const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
+    if (which == 0 && col == 0) a.q_pow[t] = ldexpf(1.0f, ex);
+    uint2 hi, lo;
+    split4(x[i], ldexpf(1.0f, -ex), hi, lo);
+    *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
+    *reinterpret_cast<uint2 *>(a.planes[which][1] + t * D + col) = lo;
+  }
+}
+
+// ---- host side -------------------------------------------------------------------------------------------
+
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+int64_t split_tiles(int64_t tokens, int32_t batch) { return tokens / kSplitRows + batch; }
+
+template <int D, int MODE>
+int launch(const Maps &maps, const Args &a, cudaStream_t s, const DevInfo &dev) {
+  using C = Cfg<D, MODE>;
+  auto kern = attn_prompt_kernel<D, MODE>;
+  static_assert(sizeof(Shared) <= 1024, "barriers");
+  static std::once_flag once[64];
+  static cudaError_t err[64];
+  std::call_once(once[dev.device], [&] {
+    err[dev.device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
+    cudaFuncAttributes fa;
+    // The helpers' registers go to the others out of what a block is launched with: it has to be all of it.
+    if (err[dev.device] == cudaSuccess) err[dev.device] = cudaFuncGetAttributes(&fa, kern);
+    if (err[dev.device] == cudaSuccess && fa.numRegs != kLaunchRegs) err[dev.device] = cudaErrorInvalidValue;
+  });
+  if (err[dev.device] != cudaSuccess) return WOQ_ECUDA;
+  const int64_t blocks = (a.tokens / kBlockRows + a.batch) * a.q_heads;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks), 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = C::Smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, maps, a) != cudaSuccess) return WOQ_ECUDA;
+  count_launches(1);
+  return WOQ_OK;
+}
+
+template <int D>
+int launch_split(const SplitArgs &a, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(a.tiles), static_cast<unsigned>(a.q.heads + 2 * a.k.heads), 1);
+  cfg.blockDim = dim3(kSplitThreads, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, attn_split_kernel<D>, a) != cudaSuccess) return WOQ_ECUDA;
+  count_launches(1);
+  return WOQ_OK;
+}
+
+// The workspace of float32 rows: six planes, then the powers of two.
+struct Layout {
+  size_t plane[3], pow[3], total;
+};
+Layout layout(int64_t tokens, int32_t batch, int32_t hq, int32_t hk, int32_t dim) {
+  Layout L;
+  const size_t t = static_cast<size_t>(tokens);
+  const size_t heads[3] = {static_cast<size_t>(hq), static_cast<size_t>(hk), static_cast<size_t>(hk)};
+  size_t at = 0;
+  for (int i = 0; i < 3; ++i) {
+    L.plane[i] = at;
+    at += 2 * up256(heads[i] * t * dim * 2);
+  }
+  const size_t tiles = static_cast<size_t>(split_tiles(tokens, batch));
+  for (int i = 0; i < 3; ++i) {
+    L.pow[i] = at;
+    at += up256(heads[i] * (i == 0 ? t : tiles) * 4);
+  }
+  L.total = at;
+  return L;
+}
+
+}  // namespace
+
+size_t attn_prompt_workspace(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                             int32_t dtype) {
+  return dtype == WOQ_F32 ? layout(tokens, batch, q_heads, kv_heads, dim).total : 0;
+}
+
+int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, int64_t tokens, const int32_t *cu,
+                       int32_t batch, int32_t dim, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
+                       const DevInfo &dev) {
+  Args a = {};
+  a.cu = cu;
+  a.tokens = tokens;
+  a.batch = batch;
+  a.q_heads = q.heads;
+  a.group = q.heads / k.heads;
+  a.scale = scale * 1.44269504088896340736f;
+  a.o = o;
+  a.v = v;
+  a.tiles = split_tiles(tokens, batch);
+  const long long lim = wait_limit_cycles();
+  a.wait_limit = lim > 0 ? lim : kWaitLimit;
+  a.stuck_wait = lim < 0 ? -lim : 0;
+  const int mode = q.dtype == WOQ_F32 ? kSplit : q.dtype == WOQ_F16 ? kF16 : kBf16;
+  const CUtensorMapDataType type =
+      mode == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  Maps maps;
+  SplitArgs sp = {};
+  const woq_rows *rows[3] = {&q, &k, &v};
+  CUtensorMap *dst[3] = {maps.q, maps.k, maps.v};
+  const Layout L = mode == kSplit ? layout(tokens, batch, q.heads, k.heads, dim) : Layout{};
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t box = i == 0 ? kRows : mode == kSplit ? kSplitRows : 128;
+    for (int p = 0; p < 2; ++p) {
+      const void *base = rows[i]->data;
+      int64_t head_stride = rows[i]->head_stride, row_stride = rows[i]->row_stride;
+      if (mode == kSplit) {
+        head_stride = tokens * dim;
+        row_stride = dim;
+        sp.planes[i][p] = reinterpret_cast<__half *>(
+            static_cast<uint8_t *>(workspace) + L.plane[i] +
+            p * up256(static_cast<size_t>(rows[i]->heads) * static_cast<size_t>(tokens) * dim * 2));
+        base = sp.planes[i][p];
+      }
+      if (!make_tensor_map_3d(&dst[i][p], type, 2, base, dim, rows[i]->heads, tokens, head_stride, row_stride, 64, box,
+                              CU_TENSOR_MAP_SWIZZLE_128B))
+        return WOQ_ECUDA;
+    }
+  }
+  if (mode == kSplit) {
+    float *pow[3];
+    for (int i = 0; i < 3; ++i) pow[i] = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.pow[i]);
+    a.q_pow = sp.q_pow = pow[0];
+    a.k_pow = sp.k_pow = pow[1];
+    a.v_pow = sp.v_pow = pow[2];
+    sp.q = q;
+    sp.k = k;
+    sp.v = v;
+    sp.cu = cu;
+    sp.tokens = tokens;
+    sp.tiles = a.tiles;
+    sp.batch = batch;
+    const int rc = dim == 128 ? launch_split<128>(sp, s) : launch_split<64>(sp, s);
+    if (rc != WOQ_OK) return rc;
+  }
+  if (dim == 128)
+    return mode == kSplit ? launch<128, kSplit>(maps, a, s, dev)
+           : mode == kF16 ? launch<128, kF16>(maps, a, s, dev)
+                          : launch<128, kBf16>(maps, a, s, dev);
+  return mode == kSplit ? launch<64, kSplit>(maps, a, s, dev)
+         : mode == kF16 ? launch<64, kF16>(maps, a, s, dev)
+                        : launch<64, kBf16>(maps, a, s, dev);
+}
+
+int read_prompt_timeout_flag(int clear, unsigned *value) {
+  unsigned v = 0;
+  if (cudaMemcpyFromSymbol(&v, g_prompt_timeout_flag, sizeof(v)) != cudaSuccess) return WOQ_ECUDA;
+  if (clear && v) {
+    const unsigned z = 0;
+    if (cudaMemcpyToSymbol(g_prompt_timeout_flag, &z, sizeof(z)) != cudaSuccess) return WOQ_ECUDA;
+  }
+  *value = v;
+  return WOQ_OK;
+}
+
+}  // namespace woq

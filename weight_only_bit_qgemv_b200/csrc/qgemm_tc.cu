@@ -1063,6 +1063,18 @@ bool make_tensor_map_2d(CUtensorMap *m, CUtensorMapDataType type, size_t esize, 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType type, size_t esize, const void *base, uint64_t cols,
+                        uint64_t mid, uint64_t rows, uint64_t mid_stride, uint64_t row_stride, uint32_t box_cols,
+                        uint32_t box_rows, CUtensorMapSwizzle swz) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {cols, mid, rows};
+  const cuuint64_t strides[2] = {mid_stride * esize, row_stride * esize};
+  const cuuint32_t box[3] = {box_cols, 1, box_rows};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, type, 3, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swz,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 GemmPlan plan_gemm_tc(int64_t m, int64_t n, int64_t k, int sm_count, size_t budget,
                       bool split) {

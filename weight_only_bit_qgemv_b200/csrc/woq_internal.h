@@ -31,6 +31,12 @@ bool make_tensor_map_2d(CUtensorMap *m, CUtensorMapDataType type, size_t esize, 
                         uint64_t cols, uint64_t rows, uint32_t box_cols, uint32_t box_rows,
                         CUtensorMapSwizzle swz);
 
+// 3-D tensor map over element (row, mid, col) at base + row * row_stride + mid * mid_stride + col (strides in
+// elements), box [box_rows, 1, box_cols]; false if the driver refuses it. (qgemm_tc.cu)
+bool make_tensor_map_3d(CUtensorMap *m, CUtensorMapDataType type, size_t esize, const void *base, uint64_t cols,
+                        uint64_t mid, uint64_t rows, uint64_t mid_stride, uint64_t row_stride, uint32_t box_cols,
+                        uint32_t box_rows, CUtensorMapSwizzle swz);
+
 // ---- qgemv.cu ----
 // FP32 CUDA-core GEMV/GEMM: y[m, n] = x[m, k] . W_hat^T for any m >= 1. Arguments
 // already validated. `pdl` launches with programmatic stream serialization.
@@ -82,6 +88,14 @@ int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, in
                     int64_t width, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
                     const DevInfo &dev);
 int read_kv4_timeout_flag(int clear, unsigned *value);
+
+// ---- attn_prompt.cu ----
+size_t attn_prompt_workspace(int64_t tokens, int32_t batch, int32_t q_heads, int32_t kv_heads, int32_t dim,
+                             int32_t dtype);
+int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, int64_t tokens, const int32_t *cu,
+                       int32_t batch, int32_t dim, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
+                       const DevInfo &dev);
+int read_prompt_timeout_flag(int clear, unsigned *value);
 
 // ---- qgemm_tc.cu ----
 // How the tensor-core path runs a problem: tile width, K-splits and workspace layout
