@@ -8,9 +8,9 @@
 // One block an SM takes 256 query rows of one head as two tiles of 128 and walks the keys in tiles of
 // BK up to the diagonal. Two warpgroups have a query tile each, a row a thread: they read the scores
 // from tensor memory, keep the row's running maximum and sum, write the weights back to
-// tensor memory (over the scores) and hold the output in registers. While one has its
-// exponentials, the tensor cores work for the other. The third group's warps: 0 copies (TMA), 1 issues
-// the matrix instructions, 2 and 3 look at the values of the tiles on the diagonal.
+// tensor memory (over the scores). While one has its
+// exponentials, the tensor cores work for the other. The third group's warps: 0 copies (TMA), 1 (and 2) issue
+// the matrix instructions, 3 looks at the values of the tiles on the diagonal.
 //
 // The output is summed in registers, not in tensor memory: each tile's product starts from zero, so that
 // sums inside the tensor cores, which cut off instead of rounding, run over BK keys at most, and so that a new
@@ -41,8 +41,7 @@ constexpr int kRows = 128;               // query rows of a warpgroup: the lanes
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kSplitRows = 64;           // rows of a float32 tile with one power of two
 constexpr int kThreads = 384;
-constexpr int kLaunchRegs = 168, kConsumerRegs = 224, kHelperRegs = 56;
-static_assert(256 * kConsumerRegs + 128 * kHelperRegs <= kThreads * kLaunchRegs, "register split");
+constexpr int kLaunchRegs = 168;
 constexpr uint32_t kTmemCols = 512;
 constexpr long long kWaitLimit = 1LL << 32;   // cycles (~2 s)
 constexpr long long kDrainLimit = 1LL << 31;
@@ -52,13 +51,20 @@ enum { kBf16 = 0, kF16 = 1, kSplit = 2 };
 template <int D, int MODE>
 struct Cfg {
   static constexpr int Parts = MODE == kSplit ? 2 : 1;       // planes of an operand
-  static constexpr int BK = MODE == kSplit ? 64 : 128;       // keys of a tile
+  // Keys of a tile. Tensor memory's 512 columns hold two outputs of D columns; the rest is for two query tiles'
+  // scores (BK columns) and, 16-bit rows, their weights (BK / 2) or, float32 rows, two tiles' scores (2 BK).
+  static constexpr int BK = MODE == kSplit ? 64 : D == 128 ? 80 : 128;
   static constexpr int Subs = D / 64;                        // 128-byte columns of a tile
   static constexpr int QBytes = Parts * kRows * D * 2;
   static constexpr int KvBytes = Parts * BK * D * 2;
   static constexpr int Room = 227 * 1024 - 2048 - 2 * QBytes;
   static constexpr int Stages = Room / KvBytes > 6 ? 6 : Room / KvBytes;
+  static_assert(MODE != kSplit || BK == kSplitRows, "one power of two a tile");
   static_assert(Stages >= 3, "keys and values of two tiles are in flight at once");
+  // Registers of a thread of the two query groups and of the helpers, out of what the block is launched with. The
+  // warps that issue matrix instructions must not spill: they set the pace.
+  static constexpr int QueryRegs = MODE == kSplit ? 216 : 200, HelperRegs = MODE == kSplit ? 72 : 104;
+  static_assert(256 * QueryRegs + 128 * HelperRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr int Smem = 2 * QBytes + Stages * KvBytes + 2048;
 };
 
@@ -81,9 +87,14 @@ struct Args {
 struct Shared {
   uint64_t q_full[2];
   uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], p_full[2], t_full[2], t_empty[2];
-  uint64_t look[kBlockRows / 64];    // the copy of a diagonal tile's values is under way
-  uint64_t looked[kBlockRows / 64];  // they are there, and finite
+  // [query tile][its scores' buffer]: 16-bit rows have one, float32 rows two. s_free, 16-bit rows: read by
+  // the query tile's warps; float32 rows: the weights in their place have been multiplied.
+  uint64_t s_full[2][2], s_free[2][2];
+  // Weights written; with float32 rows also the product before it read out, which has the place of the next.
+  uint64_t p_full[2];
+  uint64_t t_full[2];
+  uint64_t look[kBlockRows / 64 + 1];    // the copy of a diagonal tile's values is under way
+  uint64_t looked[kBlockRows / 64 + 1];  // they are there, and finite
   uint64_t looked_all;
   uint64_t drain, never;
   uint32_t tmem;
@@ -96,6 +107,12 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
 }
 
 __device__ __forceinline__ void record_timeout(volatile int *abort) {
@@ -148,16 +165,14 @@ __device__ bool find_tile(const int32_t *cu, int batch, int64_t tokens, int64_t 
   return false;
 }
 
-// Shared-memory matrix descriptors, 128-byte swizzle. Rows along the summed dimension's other side
-// (queries, keys of the first product): 8-row groups 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_rows(uint32_t saddr) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+// Shared-memory matrix descriptors, 128-byte swizzle: 8-row groups 1024 bytes apart, in the upper word that all
+// share. The lower word has the address and, where rows are the summed dimension (values), the distance of
+// the 64-element columns; queries and keys, whose rows are the other dimension, do not use it.
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t sub_bytes) {
+  return ((saddr >> 4) & 0x3FFF) | (sub_bytes >> 4) << 16;
 }
-// Values: rows are the summed dimension, 8 of them 1024 bytes apart, and 64-element columns
-// `sub_bytes` apart.
-__device__ __forceinline__ uint64_t desc_cols(uint32_t saddr, uint32_t sub_bytes) {
-  return static_cast<uint64_t>((saddr >> 4) & 0x3FFF) | (static_cast<uint64_t>(sub_bytes >> 4) << 16) |
-         (64ull << 32) | (1ull << 46) | (2ull << 61);
+__device__ __forceinline__ uint64_t desc(uint32_t low) {
+  return static_cast<uint64_t>(64u | 1u << 14 | 2u << 29) << 32 | low;
 }
 // Instruction descriptor: FP32 result, M = 128, N = n; `cols`: B's rows are the summed dimension.
 __host__ __device__ constexpr uint32_t idesc_for(int n, bool bf16, bool cols) {
@@ -165,9 +180,39 @@ __host__ __device__ constexpr uint32_t idesc_for(int n, bool bf16, bool cols) {
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 
+// A warp's wait.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, long long limit, volatile int *abort) {
+  for (int i = 0; i < 64; ++i)
+    if (__all_sync(0xffffffffu, ptx::mbar_try_wait(bar, parity))) return true;
+  return __all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, limit, abort));
+}
+
+// The same number in all lanes, for the compiler to keep in a uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 template <int MODE>
 __device__ __forceinline__ uint32_t pack(float a, float b) {
   return pack2(a, b, MODE == kBf16 ? WOQ_BF16 : WOQ_F16);
+}
+
+// Values of `keys` rows at v that are not finite, added to the output row at o: their products were left out.
+// Rolled up and in line: a call, or a pointer to the kernel's arguments, costs the whole kernel registers.
+template <int D>
+__device__ __forceinline__ void add_nonfinite(void *o, const void *v, int64_t stride, int keys, int dtype) {
+#pragma unroll 1
+  for (int j = 0; j < keys; ++j) {
+#pragma unroll 1
+    for (int i = 0; i < D; i += 4) {
+      const float4 x = load4(v, j * stride + i, dtype);
+      if (isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w)) continue;
+      float4 y = load4(o, i, dtype);
+      if (!isfinite(x.x)) y.x += x.x;
+      if (!isfinite(x.y)) y.y += x.y;
+      if (!isfinite(x.z)) y.z += x.z;
+      if (!isfinite(x.w)) y.w += x.w;
+      store4(o, i, dtype, y);
+    }
+  }
 }
 
 template <int D, int MODE>
@@ -175,7 +220,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
   using C = Cfg<D, MODE>;
   constexpr int BK = C::BK, ST = C::Stages;
-  constexpr uint32_t kScores = 0, kTile = 2 * BK;  // tensor memory columns: scores, products with the values
+  // Tensor memory columns of query tile t: scores and weights, and products with the values. float32 rows:
+  // tile j's scores are in half j & 1, and its weights in their place; 16-bit rows: the weights are behind the
+  // scores. Either way the next scores do not wait for this tile's weights.
+  constexpr uint32_t kScores = MODE == kSplit ? 2 * BK : (BK + BK / 2 + 31) / 32 * 32;
+  constexpr uint32_t kTile = 2 * kScores;
+  static_assert(kTile + 2 * D <= kTmemCols, "tensor memory");
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
@@ -184,6 +234,40 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int *abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (warp == 8 && lane == 0) {
+    for (int p = 0; p < C::Parts; ++p) {
+      ptx::prefetch_tmap(&maps.q[p]);
+      ptx::prefetch_tmap(&maps.k[p]);
+      ptx::prefetch_tmap(&maps.v[p]);
+    }
+  }
+  if (warp == 9) {
+    ptx::tmem_alloc(&sh.tmem, kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  if (warp == 1 && lane == 0) {
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&sh.q_full[i], 1);
+      for (int b = 0; b < 2; ++b) {
+        ptx::mbar_init(&sh.s_full[i][b], 1);
+        ptx::mbar_init(&sh.s_free[i][b], MODE == kSplit ? 1 : 4);
+      }
+      ptx::mbar_init(&sh.p_full[i], MODE == kSplit ? 8 : 4);
+      ptx::mbar_init(&sh.t_full[i], 1);
+    }
+    for (int i = 0; i < ST; ++i) {
+      ptx::mbar_init(&sh.kv_full[i], 1);
+      ptx::mbar_init(&sh.kv_empty[i], 1);
+    }
+    for (int i = 0; i <= kBlockRows / 64; ++i) {
+      ptx::mbar_init(&sh.look[i], 1);
+      ptx::mbar_init(&sh.looked[i], 1);
+    }
+    ptx::mbar_init(&sh.looked_all, 1);
+    ptx::mbar_init(&sh.drain, 2);
+    ptx::mbar_init(&sh.never, 1);
+    ptx::fence_mbar_init();
+  }
   ptx::pdl_wait();
   const int head = static_cast<int>(blockIdx.x % a.q_heads);
   if (warp == 0) {
@@ -198,41 +282,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       sh.nonfinite = 0;
     }
   }
-  if (warp == 1 && lane == 0) {
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh.q_full[i], 1);
-      ptx::mbar_init(&sh.s_full[i], 1);
-      ptx::mbar_init(&sh.p_full[i], 4);
-      ptx::mbar_init(&sh.t_full[i], 1);
-      ptx::mbar_init(&sh.t_empty[i], 4);
-    }
-    for (int i = 0; i < ST; ++i) {
-      ptx::mbar_init(&sh.kv_full[i], 1);
-      ptx::mbar_init(&sh.kv_empty[i], 1);
-    }
-    for (int i = 0; i < kBlockRows / 64; ++i) {
-      ptx::mbar_init(&sh.look[i], 1);
-      ptx::mbar_init(&sh.looked[i], 2);
-    }
-    ptx::mbar_init(&sh.looked_all, 2);
-    ptx::mbar_init(&sh.drain, 1);
-    ptx::mbar_init(&sh.never, 1);
-    ptx::fence_mbar_init();
-  }
-  __syncthreads();
-  const int len = sh.len, r0 = sh.r0, start = sh.start;
-  if (len == 0) {  // fewer tiles than blocks
-    ptx::pdl_launch_dependents();
-    return;
-  }
-  if (warp == 9) {
-    ptx::tmem_alloc(&sh.tmem, kTmemCols);
-    ptx::tmem_relinquish();
-  }
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
+  const int len = sh.len, r0 = sh.r0, start = sh.start;
   const uint32_t tmem = sh.tmem;
+  if (len == 0) {  // fewer tiles than blocks
+    ptx::pdl_launch_dependents();
+    if (warp == 9) ptx::tmem_dealloc(tmem, kTmemCols);
+    return;
+  }
 
   // Key tiles of the two query tiles: up to the diagonal, and not behind the last row.
   auto tiles_of = [&](int t) {
@@ -245,19 +304,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int diag = r0 / BK;  // the first tile with masked pairs
   const int kv_head = head / a.group;
 
-  bool mma_issued = false;
   int issued = 0;  // copies' slots filled so far
+  // The ring's slots in order: k 0, k 1, v 0, k 2, v 1, ...
+  auto k_slot = [](int j) { return j > 0 ? 2 * j - 1 : 0; };
+  auto v_slot = [nt](int j) { return j + 1 < nt ? 2 * j + 2 : 2 * j + 1; };
 
   if (warp >= 8) {
-    ptx::regs_dec<kHelperRegs>();
+    ptx::regs_dec<C::HelperRegs>();
     if (warp == 8) {
-      // ---- copies: q 0, k 0, q 1, v 0, k 1, v 1, ... ----
+      // ---- copies, in the order in which the matrix instructions take them ----
       if (lane == 0) {
-        for (int p = 0; p < C::Parts; ++p) {
-          ptx::prefetch_tmap(&maps.q[p]);
-          ptx::prefetch_tmap(&maps.k[p]);
-          ptx::prefetch_tmap(&maps.v[p]);
-        }
         auto query = [&](int t) {
           ptx::mbar_arrive_expect_tx(&sh.q_full[t], C::QBytes);
           for (int p = 0; p < C::Parts; ++p)
@@ -282,112 +338,122 @@ __global__ void __launch_bounds__(kThreads, 1)
         query(0);
         bool ok = kv(maps.k, 0);
         if (n1 > 0) query(1);
+#pragma unroll 1
         for (int j = 0; j < nt && ok; ++j) {
-          ok = kv(maps.v, j);
+          if (j + 1 < nt) ok = kv(maps.k, j + 1);
+          ok = ok && kv(maps.v, j);
           if (ok && j >= diag) ptx::mbar_arrive(&sh.look[j - diag]);
-          ok = ok && (j + 1 == nt || kv(maps.k, j + 1));
         }
       }
-    } else if (warp == 9) {
-      // ---- matrix instructions ----
-      if (lane == 0) {
+    } else if (warp == 9 || warp == 10) {
+      // ---- matrix instructions: the warp stays together, one lane issues. Warp 9 has the scores, warp 10 the
+      // values, so that the tensor cores have the other's instructions while one waits ----
+      {
         constexpr uint32_t kIdescS = idesc_for(BK, MODE == kBf16, false), kIdescT = idesc_for(D, MODE == kBf16, true);
         constexpr int kPlaneQ = kRows * D * 2, kPlaneK = BK * D * 2;
         bool ok = true;
-        if (a.stuck_wait > 0 && !ptx::mbar_wait_bounded(&sh.never, 0, a.stuck_wait, abort)) {  // test hook
-          record_timeout(abort);
-          ok = false;
-        }
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-          if (ok && !ptx::mbar_wait_bounded(bar, parity, a.wait_limit, abort)) {
+        auto wait_for = [&](uint64_t *bar, uint32_t parity, long long limit) {
+          if (ok && !warp_wait(bar, parity, limit, abort)) {
             record_timeout(abort);
             ok = false;
           }
           return ok;
         };
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return wait_for(bar, parity, a.wait_limit); };
+        if (a.stuck_wait > 0) wait_for(&sh.never, 0, a.stuck_wait);  // test hook
         const uint32_t q_addr = ptx::smem_u32(smem), kv_addr = ptx::smem_u32(smem_kv);
-        auto scores = [&](int t, int slot) {
-          const uint32_t d = tmem + kScores + t * BK;
-          const uint32_t q = q_addr + t * C::QBytes, k = kv_addr + slot * C::KvBytes;
-          uint32_t acc = 0;
-          auto product = [&](int pq, int pk) {
+        // Scores of tile j for the query tiles that it concerns, in one elected block: between two instructions
+        // the tensor cores wait for whatever the issuing thread does.
+        auto scores = [&](int j, bool first, bool second) {
+          const int b = MODE == kSplit ? j & 1 : 0;
+          const uint32_t d = uniform(tmem + b * BK);
+          const uint32_t q = uniform(desc_low(q_addr, 16));
+          const uint32_t k = uniform(desc_low(kv_addr + k_slot(j) % ST * C::KvBytes, 16));
+          if (ptx::elect_one()) {
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk & 3) * 32;
-              ptx::tc_mma_f16(d, desc_rows(q + pq * kPlaneQ + (kk >> 2) * kRows * 128 + off),
-                              desc_rows(k + pk * kPlaneK + (kk >> 2) * BK * 128 + off), kIdescS, acc);
-              acc = 1;
-            }
-          };
-          if constexpr (MODE == kSplit) {
-            product(1, 0);
-            product(0, 1);
-          }
-          product(0, 0);
-          mma_issued = true;
-          ptx::tc_commit(&sh.s_full[t]);
-        };
-        auto values = [&](int t, int slot) {
-          const uint32_t d = tmem + kTile + t * D, p = tmem + kScores + t * BK;
-          const uint32_t v = kv_addr + slot * C::KvBytes;
-          uint32_t acc = 0;
-          auto product = [&](int pp, int pv) {
+            for (int t = 0; t < 2; ++t) {
+              if (!(t ? second : first)) continue;
+              auto product = [&](int pq, int pk, uint32_t acc) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk) {
-              ptx::tc_mma_f16_ts(d, p + pp * (BK / 2) + kk * 8, desc_cols(v + pv * kPlaneK + kk * 2048, BK * 128),
-                                 kIdescT, acc);
-              acc = 1;
+                for (int kk = 0; kk < D / 16; ++kk)  // 16 elements are 2 units of 16 bytes
+                  ptx::tc_mma_f16(
+                      d + t * kScores,
+                      desc(q + (t * C::QBytes + pq * kPlaneQ + (kk >> 2) * kRows * 128) / 16 + (kk & 3) * 2),
+                      desc(k + (pk * kPlaneK + (kk >> 2) * BK * 128) / 16 + (kk & 3) * 2), kIdescS, kk == 0 ? acc : 1);
+              };
+              if constexpr (MODE == kSplit) {
+                product(1, 0, 0);
+                product(0, 1, 1);
+              }
+              product(0, 0, MODE == kSplit);
+              ptx::tc_commit(&sh.s_full[t][b]);
             }
-          };
-          if constexpr (MODE == kSplit) {
-            product(1, 0);
-            product(0, 1);
+            ptx::tc_commit(&sh.kv_empty[k_slot(j) % ST]);
           }
-          product(0, 0);
-          ptx::tc_commit(&sh.t_full[t]);
         };
-        // Slot number i of the ring holds k 0, v 0, k 1, v 1, ... in this order.
+        // Weights times values. 16-bit rows: added to what is there, from the second tile on; float32 rows: from
+        // zero. `last`: the tile's values are needed no more.
+        auto values = [&](int t, int j, bool last) {
+          const uint32_t d = uniform(tmem + kTile + t * D);
+          const uint32_t p = uniform(tmem + t * kScores + (MODE == kSplit ? (j & 1) * BK : BK));
+          const uint32_t v = uniform(desc_low(kv_addr + v_slot(j) % ST * C::KvBytes, BK * 128));
+          if (ptx::elect_one()) {
+            auto product = [&](int pp, int pv, uint32_t acc) {
+#pragma unroll
+              for (int kk = 0; kk < BK / 16; ++kk)  // 16 keys are 2048 bytes of values
+                ptx::tc_mma_f16_ts(d, p + pp * (BK / 2) + kk * 8, desc(v + (pv * kPlaneK + kk * 2048) / 16), kIdescT,
+                                   kk == 0 ? acc : 1);
+            };
+            if constexpr (MODE == kSplit) {
+              product(1, 0, 0);
+              product(0, 1, 1);
+            }
+            product(0, 0, MODE == kSplit ? 1 : j > 0);
+            ptx::tc_commit(&sh.t_full[t]);
+            if (MODE == kSplit) ptx::tc_commit(&sh.s_free[t][j & 1]);
+            if (last) ptx::tc_commit(&sh.kv_empty[v_slot(j) % ST]);
+          }
+        };
         auto full = [&](int i) { return wait(&sh.kv_full[i % ST], (i / ST) & 1); };
-        if (wait(&sh.q_full[0], 0) && full(0)) {
-          scores(0, 0);
-          if (n1 > 0 && wait(&sh.q_full[1], 0)) scores(1, 0);
-          ptx::tc_commit(&sh.kv_empty[0]);
-        }
-        for (int j = 0; j < nt && ok; ++j) {
-          const int vi = 2 * j + 1, ki = 2 * j + 2;
-          if (!full(vi) || (j >= diag && !wait(&sh.looked[j - diag], 0))) break;
-          bool k_there = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            const int n = t ? n1 : n0;
-            if (j >= n) continue;
-            if (!wait(&sh.p_full[t], j & 1) || !wait(&sh.t_empty[t], (j & 1) ^ 1)) break;
+        if (warp == 9) {
+#pragma unroll 1
+          for (int j = 0; j < nt && ok; ++j) {
+            const bool first = j < n0, second = j < n1;
+            if (j == 0 && !(wait(&sh.q_full[0], 0) && (!second || wait(&sh.q_full[1], 0)))) break;
+            // The place for the scores is free: tile j is the j-th (16-bit) or j / 2-th one there.
+            const int b = MODE == kSplit ? j & 1 : 0, parity = ((MODE == kSplit ? j >> 1 : j) & 1) ^ 1;
+            if (!full(k_slot(j)) || (first && !wait(&sh.s_free[0][b], parity)) ||
+                (second && !wait(&sh.s_free[1][b], parity)))
+              break;
             ptx::tc_fence_after();
-            values(t, vi % ST);
-            if (j + 1 < n) {
-              if (!k_there && !full(ki)) break;
-              k_there = true;
-              scores(t, ki % ST);
+            scores(j, first, second);
+          }
+        } else {
+#pragma unroll 1
+          for (int j = 0; j < nt && ok; ++j) {
+            if (!full(v_slot(j)) || (j >= diag && !wait(&sh.looked[j - diag], 0))) break;
+#pragma unroll 1
+            for (int t = 0; t < 2; ++t) {
+              if (j >= (t ? n1 : n0)) continue;
+              if (!wait(&sh.p_full[t], j & 1)) break;
+              ptx::tc_fence_after();
+              values(t, j, t == 1 || j >= n1);
             }
           }
-          if (!ok) break;
-          ptx::tc_commit(&sh.kv_empty[vi % ST]);
-          if (k_there) ptx::tc_commit(&sh.kv_empty[ki % ST]);
         }
-        ptx::tc_commit(&sh.drain);
+        if (ptx::elect_one()) ptx::tc_commit(&sh.drain);
       }
-    } else {
+    } else if (warp == 11) {
       // ---- values on the diagonal: what is not finite becomes 0 ----
       constexpr uint32_t kExp = MODE == kBf16 ? 0x7f807f80u : 0x7c007c00u;
       constexpr uint32_t kOne = MODE == kBf16 ? 0x00800080u : 0x04000400u;
-      const int tid = threadIdx.x - 10 * 32;
       bool ok = true;
       for (int j = diag; j < nt && ok; ++j) {
-        const int i = 2 * j + 1;
+        const int i = v_slot(j);
         // The slot's phase is this tile's from the copy's start until the tile has been looked at: only
         // then does its parity mean this tile.
-        ok = __all_sync(0xffffffffu,
-                        ptx::mbar_wait_bounded(&sh.look[j - diag], 0, a.wait_limit, abort) &&
-                            ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, a.wait_limit, abort));
+        ok = warp_wait(&sh.look[j - diag], 0, a.wait_limit, abort) &&
+             warp_wait(&sh.kv_full[i % ST], (i / ST) & 1, a.wait_limit, abort);
         if (!ok) {
           record_timeout(abort);
           break;
@@ -396,7 +462,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint4 *tile = reinterpret_cast<uint4 *>(smem_kv + (i % ST) * C::KvBytes);
         const int planes = (j + 1) * BK > len ? C::Parts : 1;
         bool mine = false, wrote = false;
-        for (int c = tid; c < planes * BK * D / 8; c += 64) {
+        #pragma unroll 4
+        for (int c = lane; c < planes * BK * D / 8; c += 32) {
           uint4 x = tile[c];
           uint32_t *w = reinterpret_cast<uint32_t *>(&x);
           uint32_t bad = 0;
@@ -423,168 +490,273 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else {
     // ---- a query tile: one row a thread ----
-    ptx::regs_inc<kConsumerRegs>();
+    ptx::regs_inc<C::QueryRegs>();
     const int t = warp >> 2;
     const int row = r0 + t * kRows + (threadIdx.x & 127);
     const int n = t ? n1 : n0;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t s_addr = tmem + lanes + kScores + t * BK, t_addr = tmem + lanes + kTile + t * D;
-    float2 o[D / 2];
-#pragma unroll
-    for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0, 0);
-    float m = -INFINITY, l = 0, alpha = 0, v_pow = 1;
-    float scale = a.scale;
-    const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
-    if constexpr (MODE == kSplit) {
-      if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
-    }
+    const uint32_t s_addr = tmem + lanes + t * kScores, t_addr = tmem + lanes + kTile + t * D;
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t parity) {
-      if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(bar, parity, a.wait_limit, abort))) {
+      if (!warp_wait(bar, parity, a.wait_limit, abort)) {
         record_timeout(abort);
         ok = false;
       }
       return ok;
     };
-    // o = o alpha + the last tile's product
-    auto accumulate = [&](int j) {
-      if (!wait(&sh.t_full[t], j & 1)) return;
-      ptx::tc_fence_after();
-      const float2 al = make_float2(alpha, alpha), vp = make_float2(v_pow, v_pow);
-#pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t x[32];
-        ptx::tmem_ld_32x32b_x32(t_addr + 32 * c, x);
-        ptx::tmem_ld_wait(x);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const float2 y = make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]));
-          float2 &z = o[16 * c + i];
-          z = MODE == kSplit ? __ffma2_rn(z, al, __fmul2_rn(y, vp)) : __ffma2_rn(z, al, y);
-        }
-      }
-      ptx::tc_fence_before();
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.t_empty[t]);
+    // The output goes by way of the query tile's place in shared memory, idle after its last scores, so that a
+    // warp's stores are whole rows: written a row a lane, they took as long as three tiles.
+    constexpr int kChunks = D * (MODE == kSplit ? 4 : 2) / 16;  // 16-byte pieces of a row
+    auto stage = [&](int r, int chunk) {
+      return reinterpret_cast<uint4 *>(smem + t * C::QBytes) + r * kChunks + (chunk ^ (r & 7));
     };
-    for (int j = 0; j < n && ok; ++j) {
-      float k_pow = 1, v_next = 1;
-      if constexpr (MODE == kSplit) {
-        const int64_t at = pow0 + min(static_cast<int64_t>(sh.tile0) + j, a.tiles - 1);
-        k_pow = __ldg(a.k_pow + at);
-        v_next = __ldg(a.v_pow + at);
+    auto write_rows = [&] {
+      __syncwarp();
+      uint8_t *out = static_cast<uint8_t *>(a.o.data);
+      constexpr int kSize = MODE == kSplit ? 4 : 2;
+#pragma unroll 4
+      for (int i = lane; i < 32 * kChunks; i += 32) {
+        const int r = (warp & 3) * 32 + i / kChunks, chunk = i % kChunks, to = r0 + t * kRows + r;
+        if (to < len)
+          *reinterpret_cast<uint4 *>(out + ((start + to) * a.o.row_stride + head * a.o.head_stride) * kSize +
+                                     16 * chunk) = *stage(r, chunk);
       }
-      if (j > 0) accumulate(j - 1);
-      if (!ok || !wait(&sh.s_full[t], j & 1)) break;
-      v_pow = v_next;
-      ptx::tc_fence_after();
-      const float c = scale * k_pow;
-      const int lim = row - j * BK;  // the last column that this row sees
-      const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
-      float mx = -INFINITY;
-      auto load = [&](int ch, uint32_t (&x)[32]) {
-        ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x);
-        ptx::tmem_ld_wait(x);
+      __syncwarp();
+      if (sh.nonfinite && row < len)
+        add_nonfinite<D>(out + ((start + row) * a.o.row_stride + head * a.o.head_stride) * kSize,
+                         static_cast<const uint8_t *>(a.v.data) +
+                             ((start + diag * BK) * a.v.row_stride + kv_head * a.v.head_stride) * kSize,
+                         a.v.row_stride, row - diag * BK + 1, a.v.dtype);
+    };
+    if constexpr (MODE != kSplit) {
+      // 16-bit rows: a tile's scores in registers, the output summed in tensor memory. The weights
+      // are taken against `ref`, a maximum that may lag behind: only when a row's maximum has grown by more
+      // than 2^8 is the row's output scaled down (by its own thread), which a few tiles at a row's
+      // start need. The largest weight is then 2^8, which both types hold.
+      float ref = 0, l = 0;
+      const float c = a.scale;
+#pragma unroll 1
+      for (int j = 0; j < n; ++j) {
+        if (!wait(&sh.s_full[t][0], j & 1)) break;
+        ptx::tc_fence_after();
+        uint32_t x[BK / 16][16];
+#pragma unroll
+        for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_32x32b_x16(s_addr + 16 * ch, x[ch]);
+#pragma unroll
+        for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_wait(x[ch]);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.s_free[t][0]);
+        const int lim = row - j * BK;  // the last column that this row sees
+        const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (32 * ch + i > lim) x[i] = 0xff800000u;
+          for (int i = 0; i < BK; ++i)
+            if (i > lim) x[i >> 4][i & 15] = 0xff800000u;
         }
-      };
-      auto top = [&](const uint32_t (&x)[32]) {
+        float mx[4];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) mx = fmaxf(mx, __uint_as_float(x[i]));
-      };
-      // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
-      float2 sum = make_float2(0, 0);
-      const float2 cc = make_float2(c, c);
-      float2 ref;
-      auto settle = [&] {
+        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(x[0][i]);
+#pragma unroll
+        for (int i = 4; i < BK; i += 8)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // pairs i + 2 k, i + 2 k + 1 (the last group has one pair for two maxima)
+            const int e = i + 2 * k;
+            if (e + 1 < BK) mx[k] = max3(mx[k], __uint_as_float(x[e >> 4][e & 15]), __uint_as_float(x[(e + 1) >> 4][(e + 1) & 15]));
+          }
         // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
-        const float m2 = fmaxf(m, fmaxf(mx * c, -3.402823466e38f));
-        const float r = (MODE == kSplit ? 13.0f : 0.0f) - m2;
-        ref = make_float2(r, r);
-        alpha = ex2(m - m2);
-        l *= alpha;
-        m = m2;
-      };
-      auto weights = [&](int ch, uint32_t (&x)[32]) {
-        uint32_t hi[16], lo[16];
+        const float m = fmaxf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c, -3.402823466e38f);
+        // The last product is complete, its weights and its sum are free to be written.
+        if (j > 0) {
+          if (!wait(&sh.t_full[t], (j - 1) & 1)) break;
+          ptx::tc_fence_after();
+        }
+        if (j == 0) {
+          ref = m;
+        } else if (__any_sync(0xffffffffu, m > ref + 8.0f)) {
+          const float next = fmaxf(ref, m), alpha = ex2(ref - next);
+          const float2 al = make_float2(alpha, alpha);
+          ref = next;
+          l *= alpha;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
-          y = make_float2(ex2(y.x), ex2(y.y));
-          sum = __fadd2_rn(sum, y);
-          hi[i] = pack<MODE>(y.x, y.y);
-          if constexpr (MODE == kSplit) {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
-            lo[i] = pack<MODE>(y.x - h.x, y.y - h.y);
+          for (int ch = 0; ch < D / 16; ++ch) {
+            uint32_t y[16];
+            ptx::tmem_ld_32x32b_x16(t_addr + 16 * ch, y);
+            ptx::tmem_ld_wait(y);
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float2 z = __fmul2_rn(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), al);
+              y[i] = __float_as_uint(z.x);
+              y[i + 1] = __float_as_uint(z.y);
+            }
+            ptx::tmem_st_32x32b_x16(t_addr + 16 * ch, y);
           }
         }
-        ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
-        if constexpr (MODE == kSplit) ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+        const float2 cc = make_float2(c, c), rr = make_float2(-ref, -ref);
+        float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
+#pragma unroll
+        for (int ch = 0; ch < BK / 16; ++ch) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float2 y =
+                __ffma2_rn(make_float2(__uint_as_float(x[ch][2 * i]), __uint_as_float(x[ch][2 * i + 1])), cc, rr);
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
+            w[i] = pack<MODE>(y.x, y.y);
+          }
+          ptx::tmem_st_32x32b_x8(s_addr + BK + 8 * ch, w);
+        }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+      }
+      if (ok && n > 0) wait(&sh.t_full[t], (n - 1) & 1);
+      if (ok && n > 0) wait(&sh.looked_all, 0);
+      if (ok && n > 0) {
+        ptx::tc_fence_after();
+        const float inv = 1.0f / l;
+#pragma unroll 1
+        for (int ch = 0; ch < D / 32; ++ch) {
+          uint32_t y[32];
+          __syncwarp();
+          ptx::tmem_ld_32x32b_x32(t_addr + 32 * ch, y);
+          ptx::tmem_ld_wait(y);
+          float o[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(y[i]) * inv;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            *stage(threadIdx.x & 127, 4 * ch + i) =
+                make_uint4(pack<MODE>(o[8 * i], o[8 * i + 1]), pack<MODE>(o[8 * i + 2], o[8 * i + 3]),
+                           pack<MODE>(o[8 * i + 4], o[8 * i + 5]), pack<MODE>(o[8 * i + 6], o[8 * i + 7]));
+        }
+        write_rows();
+      }
+    } else {
+      float2 o[D / 2];
+#pragma unroll
+      for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0, 0);
+      float m = -INFINITY, l = 0, alpha = 0, v_pow = 1;
+      float scale = a.scale;
+      const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
+      if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
+      // o = o alpha + a tile's product
+      auto accumulate = [&](int j, float alpha, float v_pow) {
+        if (!wait(&sh.t_full[t], j & 1)) return;
+        ptx::tc_fence_after();
+        const float2 al = make_float2(alpha, alpha), vp = make_float2(v_pow, v_pow);
+        uint32_t x[2][32];
+        ptx::tmem_ld_32x32b_x32(t_addr, x[0]);
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          ptx::tmem_ld_wait(x[c & 1]);
+          if (c + 1 < D / 32) ptx::tmem_ld_32x32b_x32(t_addr + 32 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 y = make_float2(__uint_as_float(x[c & 1][2 * i]), __uint_as_float(x[c & 1][2 * i + 1]));
+            float2 &z = o[16 * c + i];
+            z = __ffma2_rn(z, al, __fmul2_rn(y, vp));
+          }
+        }
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
       };
-      if constexpr (BK == 64) {
-        uint32_t x0[32], x1[32];  // both chunks are read before the weights overwrite them
-        load(0, x0);
-        load(1, x1);
+      // A tile's weights come before the tile before it is added, whose factors are kept until then.
+#pragma unroll 1
+      for (int j = 0; j < n && ok; ++j) {
+        const int64_t at = pow0 + min(static_cast<int64_t>(sh.tile0) + j, a.tiles - 1);
+        const float k_pow = __ldg(a.k_pow + at), v_next = __ldg(a.v_pow + at);
+        if (!wait(&sh.s_full[t][j & 1], (j >> 1) & 1)) break;
+        ptx::tc_fence_after();
+        const uint32_t s_addr = tmem + lanes + t * kScores + (j & 1) * BK;
+        const float alpha_last = alpha;
+        const float c = scale * k_pow;
+        const int lim = row - j * BK;  // the last column that this row sees
+        const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
+        // Four maxima and four pairs of sums, so that no addition waits for the one before.
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float2 sum[4];
+        float2 ref;
+        const float2 cc = make_float2(c, c);
+        auto start_load = [&](int ch, uint32_t (&x)[32]) { ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x); };
+        auto mask = [&](int ch, uint32_t (&x)[32]) {
+          if (masked) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * ch + i > lim) x[i] = 0xff800000u;
+          }
+        };
+        auto top = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+        };
+        auto settle = [&] {
+          const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
+          const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
+          const float r = 13.0f - m2;
+          ref = make_float2(r, r);
+          alpha = ex2(m - m2);
+          l *= alpha;
+          m = m2;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sum[i] = make_float2(0, 0);
+        };
+        // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
+        auto weights = [&](int ch, const uint32_t (&x)[32]) {
+          uint32_t hi[16], lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
+            y = make_float2(ex2(y.x), ex2(y.y));
+            sum[i & 3] = __fadd2_rn(sum[i & 3], y);
+            hi[i] = pack<MODE>(y.x, y.y);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+            const float2 rest = __fadd2_rn(y, make_float2(-h.x, -h.y));
+            lo[i] = pack<MODE>(rest.x, rest.y);
+          }
+          ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
+          ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+        };
+        uint32_t x0[32], x1[32];
+        start_load(0, x0);
+        ptx::tmem_ld_wait(x0);
+        start_load(1, x1);
+        mask(0, x0);
         top(x0);
+        ptx::tmem_ld_wait(x1);
+        mask(1, x1);  // both are read before the weights overwrite them
         top(x1);
         settle();
         weights(0, x0);
         weights(1, x1);
-      } else {
-        uint32_t x[32];
 #pragma unroll
-        for (int ch = 0; ch < BK / 32; ++ch) {
-          load(ch, x);
-          top(x);
-        }
-        settle();
-#pragma unroll
-        for (int ch = 0; ch < BK / 32; ++ch) {  // weights go to columns that have been read
-          load(ch, x);
-          weights(ch, x);
-        }
+        for (int i = 0; i < 4; ++i) l += sum[i].x + sum[i].y;
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+        if (j > 0) accumulate(j - 1, alpha_last, v_pow);
+        else if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);  // nothing to read out yet
+        v_pow = v_next;
       }
-      l += sum.x + sum.y;
-      ptx::tmem_st_wait();
-      ptx::tc_fence_before();
+      if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
+      if (ok && n > 0) wait(&sh.looked_all, 0);
+      if (ok && row < len) {
+        const float inv = 1.0f / l;
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
+#pragma unroll
+        for (int i = 0; i < D / 4; ++i)
+          *stage(threadIdx.x & 127, i) = make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
+                                                    __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y));
+      }
       __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
-    }
-    if (ok && n > 0) accumulate(n - 1);
-    if (ok && n > 0) wait(&sh.looked_all, 0);
-    if (ok && row < len) {
-      const float inv = 1.0f / l;
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
-      if (sh.nonfinite) {
-        // Values on the diagonal that are not finite, in the rows that see them.
-        for (int j = diag * BK; j <= row; ++j) {
-          const int64_t at = (start + j) * a.v.row_stride + kv_head * a.v.head_stride;
-#pragma unroll
-          for (int i = 0; i < D / 4; ++i) {
-            const float4 x = load4(a.v.data, at + 4 * i, a.v.dtype);
-            if (!isfinite(x.x)) o[2 * i].x += x.x;
-            if (!isfinite(x.y)) o[2 * i].y += x.y;
-            if (!isfinite(x.z)) o[2 * i + 1].x += x.z;
-            if (!isfinite(x.w)) o[2 * i + 1].y += x.w;
-          }
-        }
-      }
-      const int64_t at = (start + row) * a.o.row_stride + head * a.o.head_stride;
-      if constexpr (MODE == kSplit) {
-        float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(a.o.data) + at);
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(o[2 * i].x, o[2 * i].y, o[2 * i + 1].x, o[2 * i + 1].y);
-      } else {
-        uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.o.data) + at);
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i)
-          dst[i] = make_uint4(pack<MODE>(o[4 * i].x, o[4 * i].y), pack<MODE>(o[4 * i + 1].x, o[4 * i + 1].y),
-                              pack<MODE>(o[4 * i + 2].x, o[4 * i + 2].y), pack<MODE>(o[4 * i + 3].x, o[4 * i + 3].y));
-      }
+      if (ok && n > 0) write_rows();
     }
   }
 
@@ -598,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, kDrainLimit, &no_abort);
     }
   }
-  if (warp == 9 && lane == 0 && mma_issued) {
+  if (warp == 9 && lane == 0) {
     int no_abort = 0;
     ptx::mbar_wait_bounded(&sh.drain, 0, kDrainLimit, &no_abort);
   }
@@ -822,7 +994,10 @@ int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, 
   CUtensorMap *dst[3] = {maps.q, maps.k, maps.v};
   const Layout L = mode == kSplit ? layout(tokens, batch, q.heads, k.heads, dim) : Layout{};
   for (int i = 0; i < 3; ++i) {
-    const uint32_t box = i == 0 ? kRows : mode == kSplit ? kSplitRows : 128;
+    const uint32_t box = i == 0 ? kRows
+                         : mode == kSplit ? Cfg<128, kSplit>::BK  // the same for both dims
+                         : dim == 128     ? Cfg<128, kBf16>::BK
+                                          : Cfg<64, kBf16>::BK;
     for (int p = 0; p < 2; ++p) {
       const void *base = rows[i]->data;
       int64_t head_stride = rows[i]->head_stride, row_stride = rows[i]->row_stride;
