@@ -43,9 +43,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kBlocksPerSm = 4;
+constexpr int kBlocksPerSm = 3;
 constexpr int kUnit = 32;      // tokens of a unit
-constexpr int kStages = 2;     // units in a warp's ring
+constexpr int kStages = 3;     // units in a warp's ring
 constexpr int kHeads = 8;      // query heads of a pass: half the rows of a matrix instruction
 constexpr int kMinUnits = 4;   // units of a part, at least: one for each warp
 constexpr long long kWaitLimit = 1LL << 32;  // cycles (~2 s)
@@ -91,11 +91,28 @@ __device__ __forceinline__ uint32_t u32(__half2 h) { return *reinterpret_cast<co
 
 // Two codes of a word as binary16: code, and 16 * code. The masked nibble with its sign bit turned
 // over (u = code + 8) and an exponent is 1024 + u (1024 + 16 u); the subtraction is exact.
-__device__ __forceinline__ uint32_t low(uint32_t w) {
-  return u32(__hsub2(h2((w & 0x000f000fu) ^ 0x64086408u), h2(0x64086408u)));
+// (w & mask) ^ magic is one instruction if only the mask is an immediate: the magic numbers are kept in registers
+// that the compiler does not know the contents of (it made two instructions of two immediates: 128 more a unit).
+// Likewise a sum's start at zero: four registers for all instead of four moves for each.
+struct Magic {
+  uint32_t low, high;
+  float zero[4];
+  __device__ __forceinline__ Magic() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) asm volatile("mov.b32 %0, 0;" : "=f"(zero[i]));
+    asm volatile("mov.b32 %0, 0x64086408;" : "=r"(low));
+    asm volatile("mov.b32 %0, 0x64806480;" : "=r"(high));
+  }
+};
+__device__ __forceinline__ uint32_t low(uint32_t w, const Magic &m) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, 0x000f000f, %2, 0x6a;" : "=r"(u) : "r"(w), "r"(m.low));
+  return u32(__hsub2(h2(u), h2(m.low)));
 }
-__device__ __forceinline__ uint32_t high(uint32_t w) {
-  return u32(__hsub2(h2((w & 0x00f000f0u) ^ 0x64806480u), h2(0x64806480u)));
+__device__ __forceinline__ uint32_t high(uint32_t w, const Magic &m) {
+  uint32_t u;
+  asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0x6a;" : "=r"(u) : "r"(w), "r"(m.high));
+  return u32(__hsub2(h2(u), h2(m.high)));
 }
 
 // a and b as binary16 high parts and binary16 remainders: 22 bits of each.
@@ -127,6 +144,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   volatile int *abort = flags;
+  const Magic magic;
 
   if (tid == 0) {
     for (int i = 0; i < kWarps * kStages; ++i) ptx::mbar_init(&bars[i], 1);
@@ -335,10 +353,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
           float2 sum = make_float2(0, 0);
 #pragma unroll
           for (int k = 0; k < NB; ++k) {
-            float c[4] = {0, 0, 0, 0};
-            mma(c, qop[(2 * k) * 32 + lane], low(w[k]), high(w[k]), c);
+            float c[4];
+            mma(c, qop[(2 * k) * 32 + lane], low(w[k], magic), high(w[k], magic), magic.zero);
             const uint32_t w8 = w[k] >> 8;
-            mma(c, qop[(2 * k + 1) * 32 + lane], low(w8), high(w8), c);
+            mma(c, qop[(2 * k + 1) * 32 + lane], low(w8, magic), high(w8, magic), c);
             const __half2 s0 = *reinterpret_cast<const __half2 *>(&ks[0][k / 2]);
             const __half2 s1 = *reinterpret_cast<const __half2 *>(&ks[1][k / 2]);
             const float2 sc = make_float2(k & 1 ? __high2float(s0) : __low2float(s0),
@@ -476,10 +494,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
           }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            float c[4] = {0, 0, 0, 0};
+            float c[4];
             const int sh = 8 * (i >> 1);
-            auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh) : low(w >> sh); };
-            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), c);
+            auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh, magic) : low(w >> sh, magic); };
+            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), magic.zero);
             mma(c, p[1], pick(v[1][0][kb]), pick(v[1][1][kb]), c);
             acc[k][i] = __ffma2_rn(acc[k][i], al, __fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
           }
