@@ -377,7 +377,7 @@ typedef struct woq_kv4 {
  * start[b] + t - cu[b] of it, which lives in page table[b, token / page].
  *   k, v    device, [tokens, kv_heads, dim], any of the three types
  *   cu      device, int32 [batch + 1], non-decreasing; rows before cu[0] and from cu[batch] on are
- *           not touched (nor read)
+ *           not used
  *   start   device, int32 [batch]: tokens that each sequence has already; NULL for none
  *   table   device, int32 [batch, width] row-major
  * The lengths stay on the device, so that a captured call follows them. A row whose token has no

@@ -94,6 +94,35 @@ def test_append_rounds_ties_and_extremes_as_the_quantiser():
     assert np.array_equal(cache.scales.cpu().numpy().view(np.uint16), scales.view(np.uint16))
 
 
+@pytest.mark.parametrize("kind", ["scales", "codes", "sizes"])
+def test_append_next_to_the_borders_of_rounding(kind):
+    """Block maxima within 3 ulp of 7 times a binary16 midpoint, values within 4 ulp of a tie, blocks of all sizes."""
+    rng = np.random.default_rng(len(kind))
+    n, heads, dim, page = 800, 4, 128, 16
+    x = rng.uniform(-1, 1, (n, heads, dim)).astype(np.float32)
+    if kind == "scales":
+        low = rng.integers(1, 0x7B00, (n, heads, dim // 32)).astype(np.uint16).view(np.float16)
+        a = (low.astype(np.float64) + np.nextafter(low, np.float16(np.inf)).astype(np.float64)) / 2 * 7
+        a = a.astype(np.float32)
+        a = (a.view(np.int32) + rng.integers(-3, 4, a.shape).astype(np.int32)).view(np.float32)
+        x *= np.repeat(a, 32, -1)
+        x[..., ::32] = a
+    elif kind == "codes":
+        s = rng.integers(1, 0x7000, (n, heads, dim // 32)).astype(np.uint16).view(np.float16).astype(np.float32)
+        tie = ((rng.integers(-7, 7, x.shape) + 0.5) * np.repeat(s, 32, -1)).astype(np.float32)
+        x = (tie.view(np.int32) + rng.integers(-4, 5, tie.shape).astype(np.int32)).view(np.float32)
+        x[..., ::32] = 7 * s
+    else:
+        x *= np.exp(rng.uniform(-100, 10, (n, heads, 1))).astype(np.float32)
+    k = torch.from_numpy(x).cuda()
+    cache = woq.KV4Cache.empty(n // page, heads, dim, page)
+    table = np.arange(n // page)[None]
+    woq.kv4_append(cache, k, -k, ints([0, n]), ints(table))
+    codes, scales, _ = expected(k, -k, [0, n], [0], table, n // page, heads, dim, page)
+    assert np.array_equal(cache.codes.cpu().numpy(), codes)
+    assert np.array_equal(cache.scales.cpu().numpy().view(np.uint16), scales.view(np.uint16))
+
+
 def test_append_marks_blocks_it_cannot_hold():
     k = torch.randn(16, 1, 64, device="cuda")
     v = torch.randn(16, 1, 64, device="cuda")

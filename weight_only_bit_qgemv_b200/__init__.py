@@ -306,20 +306,20 @@ def _device_of(t: torch.Tensor, what: str) -> int:
 
 def _rows(t: torch.Tensor, what: str, device: int) -> _lib.WoqRows:
     """The [rows, heads, dim] tensor ``t`` as the C ABI takes it; dim contiguous."""
-    dtype = _DTYPES.get(t.dtype)
-    if dtype is None or t.dim() != 3 or t.get_device() != device or t.stride(2) != 1:
+    dtype, shape, stride = _DTYPES.get(t.dtype), t.shape, t.stride()
+    if dtype is None or len(shape) != 3 or t.get_device() != device or stride[2] != 1:
         raise ValueError(
             f"{what} must be a float32, float16 or bfloat16 tensor [rows, heads, dim] on the current CUDA device, "
             "contiguous along dim"
         )
-    n, heads, dim = t.shape
+    n, heads, dim = shape
     # the stride of a dimension of one element says nothing
-    head = t.stride(1) if heads > 1 else dim
-    return _lib.WoqRows(t.data_ptr(), dtype, heads, t.stride(0) if n > 1 else heads * head, head)
+    head = stride[1] if heads > 1 else dim
+    return _lib.WoqRows(t.data_ptr(), dtype, heads, stride[0] if n > 1 else heads * head, head)
 
 
 def _ints(t: torch.Tensor, what: str, dims: int, device: int) -> int:
-    if t.dtype != torch.int32 or t.dim() != dims or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not torch.int32 or t.get_device() != device or t.dim() != dims or not t.is_contiguous():
         raise ValueError(f"{what} must be a contiguous {dims}-D int32 tensor on the current CUDA device")
     return t.data_ptr()
 
@@ -357,13 +357,14 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Ten
     qr, kr, vr = _rows(q, "q", d), _rows(k, "k", d), _rows(v, "v", d)
     cp = _ints(cu, "cu", 1, d)
     tokens, heads, dim = q.shape
-    if k.shape != v.shape or k.shape[0] != tokens or k.shape[2] != dim or not q.dtype == k.dtype == v.dtype:
+    shape = k.shape
+    if shape != v.shape or shape[0] != tokens or shape[2] != dim or not qr.dtype == kr.dtype == vr.dtype:
         raise ValueError("q, k and v must have one type, as many rows and one dim, k and v one shape")
     if out is None:
         with torch.cuda.stream(stream):
             out = torch.zeros(q.shape, dtype=q.dtype, device=q.device)
     orow = _rows(out, "out", d)
-    if out.shape != q.shape or out.dtype != q.dtype:
+    if out.shape != q.shape or orow.dtype != qr.dtype:
         raise ValueError("out must have q's shape and type")
     batch = cu.numel() - 1
     if workspace is None:
@@ -374,7 +375,8 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Ten
     rc = _lib.lib().attn_prompt(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), tokens, cp, batch, dim,
                                 dim**-0.5 if scale is None else scale, ctypes.byref(orow), ws, nbytes,
                                 _raw_stream(stream, d))
-    _lib.check(rc, "attn_prompt")
+    if rc:
+        _lib.check(rc, "attn_prompt")
     return out
 
 
@@ -398,6 +400,9 @@ class KV4Cache:
             raise ValueError("scales must be a contiguous float16 tensor [pages, kv_heads, page, 2, dim / 32]")
         if c.device != s.device:
             raise ValueError("codes and scales must be on one device")
+        object.__setattr__(self, "kv_heads", heads)
+        object.__setattr__(self, "dim", 2 * half)
+        object.__setattr__(self, "page", page)
         object.__setattr__(self, "_desc", _lib.WoqKv4(_ptr(c), _ptr(s), pages, heads, 2 * half, page))
 
     @classmethod
@@ -409,26 +414,15 @@ class KV4Cache:
         )
 
     @property
-    def kv_heads(self) -> int:
-        return self._desc.kv_heads
-
-    @property
-    def dim(self) -> int:
-        return self._desc.dim
-
-    @property
-    def page(self) -> int:
-        return self._desc.page
-
-    @property
     def nbytes(self) -> int:
         return self.codes.numel() + 2 * self.scales.numel()
 
 def _step_args(cache, k, v, cu, table, start, what):
     d = _device_of(cache.codes, "the cache")
     c = ctypes.byref(cache._desc)
-    kr, vr = _rows(k, f"{what}: k", d), _rows(v, f"{what}: v", d)
-    if k.shape != v.shape or k.shape[1:] != (cache.kv_heads, cache.dim):
+    kr, vr = _rows(k, "k", d), _rows(v, "v", d)
+    shape = k.shape
+    if shape != v.shape or shape[1] != cache.kv_heads or shape[2] != cache.dim:
         raise ValueError(f"{what}: k and v must be [tokens, {cache.kv_heads}, {cache.dim}]")
     tp = _ints(table, "table", 2, d)
     cp = _ints(cu, "cu", 1, d)
@@ -447,7 +441,8 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tens
     d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k, v, cu, table, start, "kv4_append")
     rc = _lib.lib().kv4_append(c, ctypes.byref(kr), ctypes.byref(vr), k.shape[0], cp, sp, batch, tp, width,
                                _raw_stream(stream, d))
-    _lib.check(rc, "kv4_append")
+    if rc:
+        _lib.check(rc, "kv4_append")
 
 
 def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: torch.Tensor | None = None,
@@ -465,7 +460,8 @@ def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: to
     d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k_out, v_out, cu, table, start, "kv4_gather")
     rc = _lib.lib().kv4_gather(c, cp, sp, batch, tp, width, k_out.shape[0], ctypes.byref(kr), ctypes.byref(vr),
                                _raw_stream(stream, d))
-    _lib.check(rc, "kv4_gather")
+    if rc:
+        _lib.check(rc, "kv4_gather")
     return k_out, v_out
 
 
@@ -482,23 +478,24 @@ def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.
     (C ABI ``kv4_attn``). ``scale`` defaults to dim^-1/2; without ``workspace`` one is made for the
     call."""
     d = _device_of(cache.codes, "the cache")
-    c = ctypes.byref(cache._desc)
     qr = _rows(q, "q", d)
     if out is None:
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     orow = _rows(out, "out", d)
     lp, tp = _ints(lens, "lens", 1, d), _ints(table, "table", 2, d)
     batch, width = table.shape
-    if q.shape[0] != batch or lens.shape[0] != batch or q.shape[2] != cache.dim or out.shape != q.shape:
+    shape = q.shape
+    if shape[0] != batch or lens.shape[0] != batch or shape[2] != cache.dim or out.shape != shape:
         raise ValueError("q and out must be [batch, heads, dim] of the cache's dim, lens [batch], table [batch, width]")
     if workspace is None:
         # made, zeroed and given back on the stream that uses it
         with torch.cuda.stream(stream):
             workspace = kv4_attn_workspace(cache, q)
     ws, nbytes = _space(workspace, d)
-    rc = _lib.lib().kv4_attn(ctypes.byref(qr), c, lp, batch, tp, width, cache.dim**-0.5 if scale is None else scale,
+    rc = _lib.lib().kv4_attn(ctypes.byref(qr), ctypes.byref(cache._desc), lp, batch, tp, width, cache.dim**-0.5 if scale is None else scale,
                              ctypes.byref(orow), ws, nbytes, _raw_stream(stream, d))
-    _lib.check(rc, "kv4_attn")
+    if rc:
+        _lib.check(rc, "kv4_attn")
     return out
 
 

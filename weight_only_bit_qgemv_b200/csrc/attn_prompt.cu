@@ -822,7 +822,7 @@ __device__ __forceinline__ int exponent(float big) { return big > 0 ? max(min(il
 
 // Block (tile of 64 rows of a sequence, head of q, k or v): eight warps of eight rows, a lane four values of a row.
 template <int D>
-__global__ void __launch_bounds__(kSplitThreads) attn_split_kernel(const SplitArgs a) {
+__global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const SplitArgs a) {
   constexpr int LANES = D / 4, ROWS = 8 * LANES / 32;  // rows that a lane has
   __shared__ Place place;
   __shared__ int found;
@@ -988,7 +988,7 @@ int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, 
   const int mode = q.dtype == WOQ_F32 ? kSplit : q.dtype == WOQ_F16 ? kF16 : kBf16;
   const CUtensorMapDataType type =
       mode == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-  Maps maps;
+  Maps maps = {};
   SplitArgs sp = {};
   const woq_rows *rows[3] = {&q, &k, &v};
   CUtensorMap *dst[3] = {maps.q, maps.k, maps.v};
@@ -998,7 +998,7 @@ int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, 
                          : mode == kSplit ? Cfg<128, kSplit>::BK  // the same for both dims
                          : dim == 128     ? Cfg<128, kBf16>::BK
                                           : Cfg<64, kBf16>::BK;
-    for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < (mode == kSplit ? 2 : 1); ++p) {
       const void *base = rows[i]->data;
       int64_t head_stride = rows[i]->head_stride, row_stride = rows[i]->row_stride;
       if (mode == kSplit) {

@@ -31,28 +31,54 @@ __device__ __forceinline__ int value_halfword(int h) {
 }
 
 // One block's scale and this lane's four codes of it (eight neighbouring lanes hold the block).
-// The arithmetic is qpack's: a = max |x|, s = binary16(a / 7), code = clamp(round(x / s)).
-// a / 7 is rounded once, from 64 bits. x / s needs only a correctly rounded 32-bit quotient: s has
-// 11 significant bits, so (k + 1/2) s is exact in 24, and an x next to it differs from it by at
-// least an ulp of x, more than 2^-24 of it, while half an ulp of the quotient is at most 2^-24 of
-// it: a quotient that is not a tie cannot become one. A block with a NaN or with a scale beyond
-// binary16 becomes NaN as a whole: scale NaN, codes 0.
+// The arithmetic is qpack's, bit for bit: a = max |x|, s = binary16(a / 7), code = clamp(round(x / s), -8, 7).
+// Done as written it takes 200 instructions a row and the kernel runs at a third of the memory's rate. So both
+// quotients are approximated, and computed as written only where the approximation could round otherwise:
+//   - a * (1 / 7) is off by less than 2 ulp: written out where its 13 bits below binary16's are within 4 of a half,
+//     or where binary16 is subnormal (then the code may need the clamp, too);
+//   - x * (1 / s) + 768.5, whose last bit is 2^-14, is off by less than 2^-14: written out where its 14 fraction bits
+//     are within 1 of a whole number. Above them is round(x / s) in two's complement.
+// Written out, x / s is a correctly rounded 32-bit quotient. That is enough: s has 11 significant bits, so
+// (k + 1/2) s is exact in 24, and an x next to it differs from it by at least an ulp of x, more than 2^-24 of it,
+// while half an ulp of the quotient is at most 2^-24 of it: a quotient that is not a tie cannot become one.
+// A block with a NaN or with a scale beyond binary16 becomes NaN as a whole: scale NaN, codes 0.
 __device__ __forceinline__ uint32_t quantise(float4 x, uint16_t *scale) {
-  float a = fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w)));
-  bool bad = isnan(x.x) || isnan(x.y) || isnan(x.z) || isnan(x.w);
+  auto abs_bits = [](float f) { return __float_as_uint(f) & 0x7fffffffu; };
+  // as whole numbers, where infinity and NaN are above all others
+  uint32_t big = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
 #pragma unroll
-  for (int i = 1; i < 8; i <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, i));
-  const uint32_t mine = 0xffu << (threadIdx.x & 24);
-  bad = (__ballot_sync(0xffffffffu, bad) & mine) != 0;
-  const __half h = __double2half(__ddiv_rn(static_cast<double>(a), 7.0));
-  bad = bad || __hisinf(h);
-  *scale = bad ? 0x7fffu : __half_as_ushort(h);
+  for (int i = 1; i < 8; i <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, i));
+  const float a = __uint_as_float(big), q = a * 0.142857142857f;
+  __half h = __float2half_rn(q);
+  bool exactly = q < 6.2e-5f;
+  if (exactly || ((__float_as_uint(q) + 4u - 0x1000u) & 0x1fffu) <= 8u)
+    h = __double2half(__ddiv_rn(static_cast<double>(a), 7.0));
+  if (big >= 0x7f800000u || __hisinf(h)) {
+    *scale = 0x7fffu;
+    return 0;
+  }
+  *scale = __half_as_ushort(h);
   const float s = __half2float(h);
-  if (bad || s == 0.0f) return 0;
-  auto code = [s](float v) {
-    return static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(v, s)), -8.0f), 7.0f))) & 15u;
-  };
-  return code(x.x) | code(x.y) << 4 | code(x.z) << 8 | code(x.w) << 12;
+  float inv;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
+  const float v[4] = {x.x, x.y, x.z, x.w};
+  uint32_t code = 0, least = 0x3fffu;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t t = __float_as_uint(fmaf(v[i], inv, 768.5f));
+    least = min(least, (t + 1u) & 0x3fffu);
+    code |= (t >> 14 & 15u) << 4 * i;
+  }
+  if (exactly || least <= 2u) {
+    code = 0;
+    if (s != 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        code |= (static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(v[i], s)), -8.0f), 7.0f))) & 15u)
+                << 4 * i;
+    }
+  }
+  return code;
 }
 
 struct Place {
@@ -85,10 +111,14 @@ struct Args {
   int64_t pages, tokens, width;
   const int32_t *cu, *start, *table;
   int batch, shift, heads, chunks;  // chunks: pairs of key heads of a token
+  int64_t per;                      // pieces of a warp
 };
 
 // Lanes of a warp that work on one row: D / 4. At D = 64 the lower half has the key row, the upper
 // the value row; at D = 128 the whole warp has the key row, then the value row.
+//
+// A warp takes `per` consecutive pieces (a token's pair of heads), so that it looks a token's page up once, and
+// appending, it has the next piece's rows under way while it quantises this one's.
 template <int D, bool APPEND>
 __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
   constexpr int NB = D / 32, LANES = D / 4, ROWS = 2 * D / 128;  // ROWS: rows a lane has of each head
@@ -98,33 +128,62 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
   const int64_t items = a.tokens * a.chunks;
   const int part = lane / LANES;  // D = 64: 0 the key row, 1 the value row
   const int h = lane % LANES;     // halfword of the row, four values
-  for (int64_t item = blockIdx.x * int64_t(kThreads / 32) + (threadIdx.x >> 5); item < items;
-       item += int64_t(gridDim.x) * (kThreads / 32)) {
-    const int64_t t = item / a.chunks;
-    const int h0 = static_cast<int>(item % a.chunks) * kHeadsPerWarp;
-    const Place p = place_of(t, a.cu, a.start, a.batch, a.table, a.width, a.shift, a.pages);
-    if (!p.in || (APPEND && p.page < 0)) continue;  // warp-uniform
-    const int64_t page = int64_t(1) << a.shift;
-    float4 x[kHeadsPerWarp][ROWS];
-    uint16_t sc[kHeadsPerWarp][ROWS], w[kHeadsPerWarp][ROWS];
+  const int64_t page = int64_t(1) << a.shift;
+  const int64_t first = (blockIdx.x * int64_t(kThreads / 32) + (threadIdx.x >> 5)) * a.per;
+  const int64_t last = first + a.per < items ? first + a.per : items;
+  if (first >= last) return;
+  auto load = [&](int64_t t, int h0, float4 (&x)[kHeadsPerWarp][ROWS]) {
 #pragma unroll
-    for (int i = 0; i < kHeadsPerWarp; ++i) {
+    for (int i = 0; i < kHeadsPerWarp; ++i)
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
+        const woq_rows &src = (ROWS == 2 ? r : part) ? a.v : a.k;
         x[i][r] = make_float4(0, 0, 0, 0);
-        sc[i][r] = w[i][r] = 0;
-        const int hd = h0 + i, kv = ROWS == 2 ? r : part;
-        if (hd >= a.heads) continue;
-        if constexpr (APPEND) {
-          const woq_rows &src = kv ? a.v : a.k;
-          x[i][r] = load4(src.data, t * src.row_stride + hd * src.head_stride + 4 * h, src.dtype);
-        } else if (p.page >= 0) {
-          const int64_t base = (p.page * a.heads + hd) * 2;
-          const int at = kv ? value_halfword<D>(h) : key_halfword<D>(h);
-          w[i][r] = reinterpret_cast<const uint16_t *>(a.codes)[((base + kv) * page + p.slot) * (D / 4) + at];
-          sc[i][r] = a.scales[(base / 2 * page + p.slot) * 2 * NB + kv * NB + h / 8];
-        }
+        if (h0 + i < a.heads)
+          x[i][r] = load4(src.data, t * src.row_stride + (h0 + i) * src.head_stride + 4 * h, src.dtype);
       }
+  };
+  int64_t t = first / a.chunks;
+  int chunk = static_cast<int>(first % a.chunks);
+  float4 next[kHeadsPerWarp][ROWS];
+  if constexpr (APPEND) load(t, chunk * kHeadsPerWarp, next);
+  Place p = place_of(t, a.cu, a.start, a.batch, a.table, a.width, a.shift, a.pages);
+  for (int64_t item = first; item < last; ++item) {
+    const int h0 = chunk * kHeadsPerWarp;
+    const int64_t token = t;
+    const Place at_page = p;
+    if (++chunk == a.chunks) {
+      chunk = 0;
+      ++t;
+    }
+    float4 x[kHeadsPerWarp][ROWS];
+    if constexpr (APPEND) {
+#pragma unroll
+      for (int i = 0; i < kHeadsPerWarp; ++i)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) x[i][r] = next[i][r];
+      if (item + 1 < last) load(t, chunk * kHeadsPerWarp, next);
+    }
+    if (t != token && item + 1 < last)
+      p = place_of(t, a.cu, a.start, a.batch, a.table, a.width, a.shift, a.pages);
+    if (!at_page.in || (APPEND && at_page.page < 0)) continue;  // warp-uniform
+    // This lane's halfword and scale of the first head's key row; the others are whole pages of rows on.
+    const int64_t head0 = at_page.page < 0 ? 0 : at_page.page * a.heads + h0;
+    uint16_t *codes = reinterpret_cast<uint16_t *>(a.codes) + (head0 * 2 * page + at_page.slot) * (D / 4);
+    uint16_t *scales = a.scales + (head0 * page + at_page.slot) * 2 * NB + h / 8;
+    const int64_t row_step = page * (D / 4), scale_step = page * 2 * NB;
+    uint16_t sc[kHeadsPerWarp][ROWS], w[kHeadsPerWarp][ROWS];
+    if constexpr (!APPEND) {
+#pragma unroll
+      for (int i = 0; i < kHeadsPerWarp; ++i)
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+          const int kv = ROWS == 2 ? r : part;
+          sc[i][r] = w[i][r] = 0;
+          if (h0 + i >= a.heads || at_page.page < 0) continue;
+          w[i][r] = codes[(2 * i + kv) * row_step + (kv ? value_halfword<D>(h) : key_halfword<D>(h))];
+          sc[i][r] = scales[i * scale_step + kv * NB];
+        }
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp; ++i) {
@@ -132,19 +191,16 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
       for (int r = 0; r < ROWS; ++r) {
         const int hd = h0 + i, kv = ROWS == 2 ? r : part;
         if (hd >= a.heads) continue;  // warp-uniform
-        const int64_t base = (p.page * a.heads + hd) * 2;
         if constexpr (APPEND) {
           uint16_t s;
           const uint32_t c = quantise(x[i][r], &s);
-          const int at = kv ? value_halfword<D>(h) : key_halfword<D>(h);
-          reinterpret_cast<uint16_t *>(a.codes)[((base + kv) * page + p.slot) * (D / 4) + at] =
-              static_cast<uint16_t>(c);
-          if ((h & 7) == 0) a.scales[(base / 2 * page + p.slot) * 2 * NB + kv * NB + h / 8] = s;
+          codes[(2 * i + kv) * row_step + (kv ? value_halfword<D>(h) : key_halfword<D>(h))] = static_cast<uint16_t>(c);
+          if ((h & 7) == 0) scales[i * scale_step + kv * NB] = s;
         } else {
           const woq_rows &dst = kv ? a.v : a.k;
           const float s = __half2float(__ushort_as_half(sc[i][r]));
           const int c = static_cast<int>(w[i][r]) << 16;  // sign-extend each nibble from the top
-          store4(dst.data, t * dst.row_stride + hd * dst.head_stride + 4 * h, dst.dtype,
+          store4(dst.data, token * dst.row_stride + hd * dst.head_stride + 4 * h, dst.dtype,
                  make_float4(s * static_cast<float>(c << 12 >> 28), s * static_cast<float>(c << 8 >> 28),
                              s * static_cast<float>(c << 4 >> 28), s * static_cast<float>(c >> 28)));
         }
@@ -155,17 +211,21 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
 
 template <int D, bool APPEND>
 int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
-  const int64_t warps = a.tokens * a.chunks, per = kThreads / 32;
+  // One piece a warp while they fit the device at once, then as many waves as keep a warp at 8 at most.
+  const int64_t items = a.tokens * a.chunks, in_block = kThreads / 32;
+  Args b = a;
+  b.per = std::min<int64_t>(8, std::max<int64_t>(1, items / (int64_t(dev.sm_count) * in_block * 4)));
+  const int64_t warps = (items + b.per - 1) / b.per;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(std::min<int64_t>((warps + per - 1) / per, int64_t(dev.sm_count) * 8)), 1, 1);
+  cfg.gridDim = dim3(static_cast<unsigned>((warps + in_block - 1) / in_block), 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, APPEND>, a) != cudaSuccess) return WOQ_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, APPEND>, b) != cudaSuccess) return WOQ_ECUDA;
   count_launches(1);
   return WOQ_OK;
 }
