@@ -363,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.stuck_wait > 0) wait_for(&sh.never, 0, a.stuck_wait);  // test hook
         const uint32_t q_addr = ptx::smem_u32(smem), kv_addr = ptx::smem_u32(smem_kv);
         // Scores of tile j for the query tiles that it concerns, in one elected block: between two instructions
-        // the tensor cores wait for whatever the issuing thread does.
-        auto scores = [&](int j, bool first, bool second) {
+        // the tensor cores wait for whatever the issuing thread does. `last`: the tile's keys are needed no more.
+        auto scores = [&](int j, bool first, bool second, bool last) {
           const int b = MODE == kSplit ? j & 1 : 0;
           const uint32_t d = uniform(tmem + b * BK);
           const uint32_t q = uniform(desc_low(q_addr, 16));
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               product(0, 0, MODE == kSplit);
               ptx::tc_commit(&sh.s_full[t][b]);
             }
-            ptx::tc_commit(&sh.kv_empty[k_slot(j) % ST]);
+            if (last) ptx::tc_commit(&sh.kv_empty[k_slot(j) % ST]);
           }
         };
         // Weights times values. 16-bit rows: added to what is there, from the second tile on; float32 rows: from
@@ -419,14 +419,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int j = 0; j < nt && ok; ++j) {
             const bool first = j < n0, second = j < n1;
-            if (j == 0 && !(wait(&sh.q_full[0], 0) && (!second || wait(&sh.q_full[1], 0)))) break;
             // The place for the scores is free: tile j is the j-th (16-bit) or j / 2-th one there.
             const int b = MODE == kSplit ? j & 1 : 0, parity = ((MODE == kSplit ? j >> 1 : j) & 1) ^ 1;
             if (!full(k_slot(j)) || (first && !wait(&sh.s_free[0][b], parity)) ||
                 (second && !wait(&sh.s_free[1][b], parity)))
               break;
+            if (j == 0 && !(wait(&sh.q_full[0], 0) && (!second || wait(&sh.q_full[1], 0)))) break;
             ptx::tc_fence_after();
-            scores(j, first, second);
+            scores(j, first, second, true);
           }
         } else {
 #pragma unroll 1
@@ -461,15 +461,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The high plane; the other is finite in the sequence's rows, and unknown behind them.
         uint4 *tile = reinterpret_cast<uint4 *>(smem_kv + (i % ST) * C::KvBytes);
         const int planes = (j + 1) * BK > len ? C::Parts : 1;
-        bool mine = false, wrote = false;
-        #pragma unroll 4
-        for (int c = lane; c < planes * BK * D / 8; c += 32) {
-          uint4 x = tile[c];
-          uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-          uint32_t bad = 0;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) bad |= (w[k] & kExp) + kOne;
-          if (bad & 0x80008000u) {
+        // Exponents of ones only, in two halves of a word at once: adding one to such an exponent sets the sign.
+        auto check = [](const uint4 &x) {
+          return (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) &
+                 0x80008000u;
+        };
+        const int pieces = planes * BK * D / 8;
+        uint32_t bad = 0;
+#pragma unroll 8
+        for (int c = lane; c < pieces; c += 32) bad |= check(tile[c]);
+        if (__any_sync(0xffffffffu, bad != 0)) {
+          bool mine = false;
+          for (int c = lane; c < pieces; c += 32) {
+            uint4 x = tile[c];
+            if (!check(x)) continue;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t b = ((w[k] & kExp) + kOne) & 0x80008000u;
@@ -477,12 +483,11 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (b & 0x80000000u) w[k] &= 0xffffu;
             }
             tile[c] = x;
-            wrote = true;
             mine |= j * BK + c / 8 % BK < len;  // not of the rows behind the sequence
           }
+          if (mine) sh.nonfinite = 1;
+          ptx::fence_proxy_async_smem();
         }
-        if (mine) sh.nonfinite = 1;
-        if (wrote) ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&sh.looked[j - diag]);
       }
