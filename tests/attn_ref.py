@@ -35,7 +35,8 @@ def read_pages(codes, scales):
     nib = np.where(nib > 7, nib - 16, nib)
     at = halfword_places(2 * half)
     s = np.repeat(scales, 32, axis=-1)
-    return np.stack([nib[:, :, i][..., at[i]] * s[:, :, :, i] for i in (0, 1)])
+    with np.errstate(invalid="ignore"):  # 0 times an infinite scale
+        return np.stack([nib[:, :, i][..., at[i]] * s[:, :, :, i] for i in (0, 1)])
 
 
 def write_pages(q, s, i, codes, scales, page, slot):

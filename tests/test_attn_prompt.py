@@ -181,6 +181,17 @@ def test_strides_and_neighbours():
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+def test_rows_of_heads_stored_head_after_head(dtype):
+    q, k, v = fused(13, 300, 4, 2, 64, dtype)
+    want = woq.attn_prompt(q, k, v, ints([0, 300]))
+    q, k, v = (x.transpose(0, 1).contiguous().transpose(0, 1) for x in (q, k, v))
+    out = torch.empty(4, 300, 64, dtype=dtype, device="cuda").transpose(0, 1)
+    assert torch.equal(woq.attn_prompt(q, k, v, ints([0, 300]), out=out), want)
+    with pytest.raises(woq.WoqError):
+        woq.attn_prompt(q[:, :1].expand(-1, 4, -1), k, v, ints([0, 300]))  # a stride of 0
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_same_bits_every_time_captured_and_on_another_stream(dtype):
     cu = ints([0, 700, 900])
     q, k, v = fused(10, 900, 4, 2, 128, dtype)

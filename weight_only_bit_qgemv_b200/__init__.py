@@ -332,9 +332,14 @@ def _space(workspace: torch.Tensor | None, device: int) -> tuple[int | None, int
     return workspace.data_ptr(), workspace.nbytes
 
 
+# The current stream's handle alone: a torch.cuda.Stream object for it costs as much as the rest of a call.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream
+)
+
+
 def _raw_stream(stream, device: int) -> int:
-    # the handle alone: a torch.cuda.Stream object for it costs as much as the rest of a call
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    return _current_raw_stream(device) if stream is None else stream.cuda_stream
 
 
 def attn_prompt_workspace(q: torch.Tensor, k: torch.Tensor, batch: int) -> torch.Tensor | None:
