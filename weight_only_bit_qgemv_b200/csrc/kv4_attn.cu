@@ -45,7 +45,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlocksPerSm = 3;
 constexpr int kUnit = 32;      // tokens of a unit
-constexpr int kStages = 3;     // units in a warp's ring
+constexpr int kStages = 2;     // units in a warp's ring
 constexpr int kHeads = 8;      // query heads of a pass: half the rows of a matrix instruction
 constexpr int kMinUnits = 4;   // units of a part, at least: one for each warp
 constexpr long long kWaitLimit = 1LL << 32;  // cycles (~2 s)
@@ -133,10 +133,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   using S = Shape<D>;
   constexpr int NB = S::NB;
   extern __shared__ __align__(128) uint8_t smem[];
-  // [ring: kWarps * kStages * Stage][q operands: 2 NB * 32 * 16][bars][fac, flags][prefix]
+  // [ring: kWarps * kStages * Stage][q operands: 2 NB * 32 * 16][results: kWarps * Slot][bars][fac, flags][prefix]
   uint8_t *ring = smem;
   uint4 *qop = reinterpret_cast<uint4 *>(smem + kWarps * kStages * S::Stage);
-  uint64_t *bars = reinterpret_cast<uint64_t *>(qop + 2 * NB * 32);
+  float *results = reinterpret_cast<float *>(qop + 2 * NB * 32);
+  uint64_t *bars = reinterpret_cast<uint64_t *>(results + kWarps * S::Slot);
   float *fac = reinterpret_cast<float *>(bars + kWarps * kStages);   // [kHeads]
   int *flags = reinterpret_cast<int *>(fac + kHeads);                // abort, last
   int64_t *pre = reinterpret_cast<int64_t *>(flags + 4);             // [batch + 1]: units before a sequence
@@ -196,55 +197,65 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   uint8_t *mine = ring + warp * kStages * S::Stage;
   uint64_t *bar = bars + warp * kStages;
 
-  for (int64_t cur = begin; cur < end;) {
-    // The sequence, key head and chunk of unit `cur`.
+  // A unit's copies: lane 2 i + h of the first six has the 16 tokens of half h, i = 0 their keys,
+  // 1 values, 2 scales, and keeps the table's entry of its half for the unit that is next to copy.
+  const int half = lane & 1, what = lane >> 1, page = 1 << a.shift;
+  const int unit_bytes = what == 2 ? S::ScaleBytes : S::RowBytes;
+  const int64_t page_bytes = int64_t(a.kv_heads) * page * (what == 2 ? S::ScaleBytes : 2 * S::RowBytes);
+  uint8_t *into = mine + what * S::Values + 16 * half * unit_bytes;
+  const uint32_t pages = static_cast<uint32_t>(a.pages);  // an entry outside, or negative, is no page
+  int b = 0, units = 0, pass = 0, u_begin = 0, u_end = 0, len = 0, kvh = 0;
+  const int32_t *row = a.table;
+  const uint8_t *pool = a.codes;
+  int32_t next = -1;     // the entry
+  uint32_t there = 0;    // halves that have a page, of the units in the ring: 2 bits each, oldest first
+  auto entry = [&](int u) -> int32_t {
+    const uint32_t key = static_cast<uint32_t>(u) * kUnit + 16 * half;
+    return u < u_end && key < static_cast<uint32_t>(len) ? row[key >> a.shift] : -1;
+  };
+  auto issue = [&](int u, int st, int32_t e) {
+    const bool good = static_cast<uint32_t>(e) < pages;
+    const uint32_t halves = __ballot_sync(0xffffffffu, good) & 3u;
+    there = there >> 2 | halves << 2 * (kStages - 1);
+    if (u >= u_end) return;
+    if (lane == 0) ptx::mbar_arrive_expect_tx(&bar[st], __popc(halves) * (S::Stage / 2));
+    if (lane < 6 && good) {
+      const uint32_t slot = (static_cast<uint32_t>(u) * kUnit + 16 * half) & (page - 1);
+      ptx::bulk_load(into + st * S::Stage, pool + e * page_bytes + slot * unit_bytes, 16 * unit_bytes, &bar[st]);
+    }
+  };
+  // The sequence, key head and chunk of unit `cur`, and the copies of this warp's first units there. A sequence has
+  // less than 2^31 tokens, so its units and their tokens fit 32 bits.
+  auto enter = [&](int64_t cur) {
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (pre[mid] * heads <= cur) lo = mid;
       else hi = mid;
     }
-    const int b = lo;
-    // a sequence has less than 2^31 tokens, so its units and their tokens fit 32 bits
-    const int units = static_cast<int>(pre[b + 1] - pre[b]);
+    b = lo;
+    units = static_cast<int>(pre[b + 1] - pre[b]);
     const int64_t at = cur - pre[b] * heads;
-    const int pass = static_cast<int>(at / units);
-    const int u_begin = static_cast<int>(at % units);
-    const int u_end = u_begin + static_cast<int>(end - cur < units - u_begin ? end - cur : units - u_begin);
-    const int kvh = pass / a.chunks, h0 = (pass % a.chunks) * kHeads;
-    const int nh = a.group - h0 < kHeads ? a.group - h0 : kHeads;
-    const int64_t len = a.lens[b] > longest ? longest : a.lens[b];
+    pass = static_cast<int>(at / units);
+    u_begin = static_cast<int>(at % units);
+    u_end = u_begin + static_cast<int>(end - cur < units - u_begin ? end - cur : units - u_begin);
+    kvh = pass / a.chunks;
+    len = static_cast<int>(a.lens[b] > longest ? longest : a.lens[b]);
+    row = a.table + b * a.width;
+    pool = what == 2 ? a.scales + int64_t(kvh) * page * S::ScaleBytes
+                     : a.codes + (int64_t(kvh) * 2 + what) * page * S::RowBytes;
+    int32_t e[kStages];
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) e[i] = entry(u_begin + warp + i * kWarps);
+    next = entry(u_begin + warp + kStages * kWarps);
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) issue(u_begin + warp + i * kWarps, i, e[i]);
+  };
+  if (begin < end) enter(begin);
 
-    // A unit's copies: lane 2 i + h of the first six has the 16 tokens of half h, i = 0 their keys,
-    // 1 values, 2 scales, and keeps the table's entries of its half for the units ahead.
-    const int half = lane & 1, what = lane >> 1;
-    const int32_t *row = a.table + b * a.width;
-    const int page = 1 << a.shift;
-    const int unit_bytes = what == 2 ? S::ScaleBytes : S::RowBytes;
-    const int64_t page_bytes = int64_t(a.kv_heads) * page * (what == 2 ? S::ScaleBytes : 2 * S::RowBytes);
-    const uint8_t *pool = what == 2 ? a.scales + int64_t(kvh) * page * S::ScaleBytes
-                                    : a.codes + (int64_t(kvh) * 2 + what) * page * S::RowBytes;
-    uint8_t *into = mine + what * S::Values + 16 * half * unit_bytes;
-    auto entry = [&](int u) -> int32_t {
-      const int64_t key = int64_t(u) * kUnit + 16 * half;
-      return u < u_end && key < len ? row[key >> a.shift] : -1;
-    };
-    auto good = [&](int32_t e) { return e >= 0 && e < a.pages; };
-    auto issue = [&](int u, int st, int32_t e) {
-      const uint32_t halves = __popc(__ballot_sync(0xffffffffu, good(e)) & 3u);
-      if (u >= u_end) return;
-      if (lane == 0) ptx::mbar_arrive_expect_tx(&bar[st], halves * (S::Stage / 2));
-      if (lane < 6 && good(e)) {
-        const uint32_t slot = (static_cast<uint32_t>(u) * kUnit + 16 * half) & (page - 1);
-        ptx::bulk_load(into + st * S::Stage, pool + e * page_bytes + slot * unit_bytes, 16 * unit_bytes, &bar[st]);
-      }
-    };
-    const int u0 = u_begin + warp;
-    int32_t e[kStages + 1];  // entries of the units in the ring and of the one after
-#pragma unroll
-    for (int i = 0; i <= kStages; ++i) e[i] = entry(u0 + i * kWarps);
-#pragma unroll
-    for (int i = 0; i < kStages; ++i) issue(u0 + i * kWarps, i, e[i]);
+  for (int64_t cur = begin; cur < end;) {
+    const int h0 = (pass % a.chunks) * kHeads;
+    const int nh = a.group - h0 < kHeads ? a.group - h0 : kHeads;
 
     // The query: rows h0 .. h0 + nh - 1 of this key head, times scale * log2(e), times the power of two
     // that brings the row's largest into [2^13, 2^14).
@@ -304,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 
     int st = 0;
     bool ok = true;
-    for (int u = u0; u < u_end; u += kWarps) {
+    for (int u = u_begin + warp; u < u_end; u += kWarps) {
       if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(&bar[st], phases >> st & 1, a.wait_limit, abort))) {
         *abort = 1;
         atomicOr(&g_kv4_timeout_flag, 1u);
@@ -315,8 +326,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       const uint8_t *base = mine + st * S::Stage;
 
       // Tokens of each half that are there: all 32, as a rule.
-      const uint32_t pages_ok = __ballot_sync(0xffffffffu, good(e[0])) & 3u;
-      const int64_t rest = len - int64_t(u) * kUnit;
+      const uint32_t pages_ok = there & 3u;
+      const int rest = len - u * kUnit;
       const bool full = pages_ok == 3u && rest >= kUnit;
 
       // ---- scores: two matrices of 8 tokens for each half of the unit ----
@@ -363,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
                                           k & 1 ? __high2float(s1) : __low2float(s1));
             sum = __ffma2_rn(__fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])), sc, sum);
           }
-          s[h][i] = __fmul2_rn(sum, make_float2(f, f));
+          s[h][i] = sum;  // times f below
         }
       }
       if (!full) {  // warp-uniform: tokens that are not there weigh nothing, whatever the stage holds
@@ -439,9 +450,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
       // Any token makes the maximum finite, so that -infinity means that there was none: a row of
       // scores that are all NaN or -infinity gives NaN, as the formula does.
+      mx *= f;
       if (pages_ok) mx = fmaxf(mx, -3.402823466e38f);
       const float m2 = fmaxf(m, mx);
-      const float ref = (m2 == -INFINITY ? 0.0f : m2) - 6.0f;
+      const float ref = 6.0f - (m2 == -INFINITY ? 0.0f : m2);
       const float beta = m == -INFINITY ? -INFINITY : m - m2;
       const float alpha = ex2(beta + shift);
       l *= ex2(beta);
@@ -450,9 +462,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          s[h][i] = make_float2(ex2(s[h][i].x - ref), ex2(s[h][i].y - ref));
-          l += s[h][i].x + s[h][i].y;
+          const float2 y = __ffma2_rn(s[h][i], make_float2(f, f), make_float2(ref, ref));
+          s[h][i] = make_float2(ex2(y.x), ex2(y.y));
         }
+      const float2 sum = __fadd2_rn(__fadd2_rn(s[0][0], s[0][1]), __fadd2_rn(s[1][0], s[1][1]));
+      l += sum.x + sum.y;
 
       // ---- values ----
       const float2 al = make_float2(alpha, alpha);
@@ -505,23 +519,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       }
 
       __syncwarp();  // every lane has read the stage
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) e[i] = e[i + 1];
-      issue(u + kStages * kWarps, st, e[kStages - 1]);
-      e[kStages] = entry(u + (kStages + 1) * kWarps);
+      issue(u + kStages * kWarps, st, next);
+      next = entry(u + (kStages + 1) * kWarps);
       st = st + 1 == kStages ? 0 : st + 1;
     }
-    if (!ok) {
-      // The copies that this warp still has in flight end before the block does.
-      int never = 0;
-      for (int i = 0; i < kStages; ++i) ptx::mbar_wait_bounded(&bar[i], phases >> i & 1, 1LL << 28, &never);
-    }
+    // This segment, and into the next one's: its copies are under way while this one's results are put together.
+    const int this_b = b, this_kvh = kvh, this_pass = pass, this_units = units;
+    const int64_t after = cur + (u_end - u_begin);
+    __syncwarp();
+    if (ok && after < end) enter(after);
 
     // ---- the four warps' results, then the block's ----
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    __syncthreads();  // the ring is idle: it takes the warps' results
-    float *res = reinterpret_cast<float *>(ring) + warp * S::Slot;
+    float *res = results + warp * S::Slot;
     if (t == 0) {
       res[kHeads * D + g] = m;
       res[kHeads * D + kHeads + g] = l;
@@ -570,14 +581,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
       for (int i = 0; i < ND; ++i)
         store4(a.o.data,
-               b * a.o.row_stride + (static_cast<int64_t>(kvh) * a.group + h0 + hd) * a.o.head_stride + d0 + 64 * i,
+               this_b * a.o.row_stride + (static_cast<int64_t>(this_kvh) * a.group + h0 + hd) * a.o.head_stride + d0 +
+                   64 * i,
                a.o.dtype, make_float4(o[i].x * r, o[i].y * r, o[i].z * r, o[i].w * r));
     };
     reset();
     for (int k = 0; k < kWarps; ++k)
-      add(reinterpret_cast<const float *>(ring) + k * S::Slot, [](const float *p) { return *p; },
+      add(results + k * S::Slot, [](const float *p) { return *p; },
           [](const float *p) { return *reinterpret_cast<const float4 *>(p); });
-    const int64_t first = pre[b] * heads + pass * units, last = first + units - 1;  // units of this pass
+    const int64_t first = pre[this_b] * heads + int64_t(this_pass) * this_units;
+    const int64_t last = first + this_units - 1;  // units of this pass
     if (first >= begin && last < end) {
       finish();
     } else {
@@ -592,7 +605,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       }
       __threadfence();
       __syncthreads();
-      unsigned *counter = a.counters + static_cast<int64_t>(b) * heads + pass;
+      unsigned *counter = a.counters + static_cast<int64_t>(this_b) * heads + this_pass;
       if (tid == 0) flags[1] = atomicAdd(counter, 1u) == static_cast<unsigned>(x1 - x0);
       __syncthreads();
       if (flags[1]) {
@@ -609,11 +622,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         finish();
       }
     }
-    // The next segment's copies (the async proxy) overwrite what was written and read here.
-    ptx::fence_proxy_async_smem();
-    __syncthreads();
-    cur += u_end - u_begin;
-    if (*abort) break;  // uniform: read behind a barrier, written before it
+    __syncthreads();  // the results and the query's operands are read
+    cur = after;
+    if (*abort) {  // uniform: read behind a barrier, written before it
+      // The copies that this warp still has in flight end before the block does (or the wait for none gives up).
+      int never = 0;
+      for (int i = 0; i < kStages; ++i) ptx::mbar_wait_bounded(&bar[i], phases >> i & 1, 1LL << 28, &never);
+      break;
+    }
   }
   ptx::pdl_launch_dependents();
 }
@@ -621,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 template <int D>
 size_t smem_bytes(int batch) {
   using S = Shape<D>;
-  return static_cast<size_t>(kWarps) * kStages * S::Stage + 2 * S::NB * 32 * 16 + kWarps * kStages * 8 +
+  return static_cast<size_t>(kWarps) * (kStages * S::Stage + S::Slot * 4) + 2 * S::NB * 32 * 16 + kWarps * kStages * 8 +
          (kHeads + 4) * 4 + 8 * (static_cast<size_t>(batch) + 1);
 }
 
