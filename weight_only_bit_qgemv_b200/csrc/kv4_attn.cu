@@ -58,7 +58,11 @@ struct Shape {
   static constexpr int Values = kUnit * RowBytes;     // a stage: keys, values, scales of 32 tokens
   static constexpr int Scales = 2 * kUnit * RowBytes;
   static constexpr int Stage = kUnit * (2 * RowBytes + ScaleBytes);
-  static constexpr int Slot = kHeads * (D + 2);       // floats of a partial result
+  // A partial result, floats: the heads' sums (rows four apart, so that eight heads' are in different banks),
+  // their maxima and their totals.
+  static constexpr int HeadStep = D + 4;
+  static constexpr int Maxima = kHeads * HeadStep, Totals = Maxima + kHeads;
+  static constexpr int Slot = Totals + kHeads;
 };
 
 struct Args {
@@ -207,6 +211,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   int b = 0, units = 0, pass = 0, u_begin = 0, u_end = 0, len = 0, kvh = 0;
   const int32_t *row = a.table;
   const uint8_t *pool = a.codes;
+  float query[kHeads / kWarps][NB];
   int32_t next = -1;     // the entry
   uint32_t there = 0;    // halves that have a page, of the units in the ring: 2 bits each, oldest first
   auto entry = [&](int u) -> int32_t {
@@ -244,6 +249,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     row = a.table + b * a.width;
     pool = what == 2 ? a.scales + int64_t(kvh) * page * S::ScaleBytes
                      : a.codes + (int64_t(kvh) * 2 + what) * page * S::RowBytes;
+    // the query's rows h0 .. h0 + nh - 1, under way with the table's entries
+    const int h0 = (pass % a.chunks) * kHeads;
+#pragma unroll
+    for (int i = 0; i < kHeads / kWarps; ++i) {
+      const int r = warp + i * kWarps;
+      const int64_t base = b * a.q.row_stride + (static_cast<int64_t>(kvh) * a.group + h0 + r) * a.q.head_stride;
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {  // lane = element of block k
+        query[i][k] = 0;
+        if (h0 + r < a.group) {
+          const int64_t at = base + 32 * k + lane;
+          query[i][k] = a.q.dtype == WOQ_F32   ? static_cast<const float *>(a.q.data)[at]
+                        : a.q.dtype == WOQ_F16 ? __half2float(static_cast<const __half *>(a.q.data)[at])
+                                               : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q.data)[at]);
+        }
+      }
+    }
     int32_t e[kStages];
 #pragma unroll
     for (int i = 0; i < kStages; ++i) e[i] = entry(u_begin + warp + i * kWarps);
@@ -257,22 +279,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     const int h0 = (pass % a.chunks) * kHeads;
     const int nh = a.group - h0 < kHeads ? a.group - h0 : kHeads;
 
-    // The query: rows h0 .. h0 + nh - 1 of this key head, times scale * log2(e), times the power of two
-    // that brings the row's largest into [2^13, 2^14).
-    for (int r = warp; r < kHeads; r += kWarps) {
-      float v[D / 32];
-      float big = 0;
-      const int64_t base = b * a.q.row_stride + (static_cast<int64_t>(kvh) * a.group + h0 + r) * a.q.head_stride;
+    // The query times scale * log2(e), times the power of two that brings the row's largest into [2^13, 2^14).
 #pragma unroll
-      for (int i = 0; i < NB; ++i) {  // lane = element of block i
-        float x = 0;
-        if (r < nh) {
-          const int64_t p = base + 32 * i + lane;
-          x = a.q.dtype == WOQ_F32   ? static_cast<const float *>(a.q.data)[p]
-              : a.q.dtype == WOQ_F16 ? __half2float(static_cast<const __half *>(a.q.data)[p])
-                                     : __bfloat162float(static_cast<const __nv_bfloat16 *>(a.q.data)[p]);
-        }
-        v[i] = x * a.scale;
+    for (int n = 0; n < kHeads / kWarps; ++n) {
+      const int r = warp + n * kWarps;
+      float (&v)[NB] = query[n];
+      float big = 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        v[i] *= a.scale;
         big = fmaxf(big, fabsf(v[i]));
       }
 #pragma unroll
@@ -283,14 +298,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
       for (int i = 0; i < NB; ++i) {
         v[i] *= up;
-        // Element `lane` = 8 tt + n of the block: matrix step 2 i + (n / 2 % 2), a or second pair by n % 2,
-        // first or second of the pair by n / 4; odd n meet codes 16 times too large.
-        const int n = lane & 7, tt = lane >> 3;
-        const float x = n & 1 ? v[i] * 0.0625f : v[i];
+        // Element `lane` = 8 tt + e of the block: matrix step 2 i + (e / 2 % 2), a or second pair by e % 2,
+        // first or second of the pair by e / 4; odd e meet codes 16 times too large.
+        const int e = lane & 7, tt = lane >> 3;
+        const float x = e & 1 ? v[i] * 0.0625f : v[i];
         const __half h = __float2half_rn(x);
         const __half l = __float2half_rn(x - __half2float(h));
-        __half *dst = reinterpret_cast<__half *>(qop + (2 * i + (n >> 1 & 1)) * 32 + (r * 4 + tt)) +
-                      4 * (n & 1) + (n >> 2);
+        __half *dst = reinterpret_cast<__half *>(qop + (2 * i + (e >> 1 & 1)) * 32 + (r * 4 + tt)) +
+                      4 * (e & 1) + (e >> 2);
         dst[0] = h;  // .x / .z: high parts (rows 0..7)
         dst[2] = l;  // .y / .w: low parts (rows 8..15)
       }
@@ -534,46 +549,57 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     float *res = results + warp * S::Slot;
     if (t == 0) {
-      res[kHeads * D + g] = m;
-      res[kHeads * D + kHeads + g] = l;
+      res[S::Maxima + g] = m;
+      res[S::Totals + g] = l;
     }
+    const float even = ldexpf(1.0f, -room), odd = 0.0625f * even;
 #pragma unroll
-    for (int k = 0; k < NB; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float unit = ldexpf(i & 1 ? 0.0625f : 1.0f, -room);
-        res[g * D + 32 * k + 8 * t + i] = acc[k][i].x * unit;
-        res[g * D + 32 * k + 8 * t + 4 + i] = acc[k][i].y * unit;
-      }
+    for (int k = 0; k < NB; ++k) {
+      float4 *to = reinterpret_cast<float4 *>(res + g * S::HeadStep + 32 * k + 8 * t);
+      to[0] = make_float4(acc[k][0].x * even, acc[k][1].x * odd, acc[k][2].x * even, acc[k][3].x * odd);
+      to[1] = make_float4(acc[k][0].y * even, acc[k][1].y * odd, acc[k][2].y * even, acc[k][3].y * odd);
+    }
     __syncthreads();
 
     // Thread: head tid / 16, D / 16 dims from (tid % 16) * 4 on, 64 apart.
     const int hd = tid >> 4, d0 = (tid & 15) * 4;
     constexpr int ND = D / 64;
-    // Adds one result (a warp's or a part's) to the running one, in the order of the calls.
-    float M = -INFINITY, L = 0;
+    // Adds up `n` results (the warps' or parts') in their order; `at(k)`: the k-th. Four results' loads are
+    // under way at once: one after the other took longer than all else of a short context.
+    float M, L;
     float4 o[ND];
-    auto reset = [&] {
+    auto join = [&](int64_t n, auto at, auto ld, auto ld4) {
       M = -INFINITY;
       L = 0;
 #pragma unroll
       for (int i = 0; i < ND; ++i) o[i] = make_float4(0, 0, 0, 0);
-    };
-    auto add = [&](const float *r, auto ld, auto ld4) {
-      const float mk = ld(r + kHeads * D + hd), lk = ld(r + kHeads * D + kHeads + hd);
-      if (mk == -INFINITY) return;  // no token seen
-      const float M2 = fmaxf(M, mk);
-      const float x = M == -INFINITY ? 0.0f : ex2(M - M2), y = ex2(mk - M2);
-      L = L * x + lk * y;
+      for (int64_t k0 = 0; k0 < n; k0 += 4) {
+        float mk[4], lk[4];
+        float4 v[4][ND];
 #pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        const float4 v = ld4(r + hd * D + d0 + 64 * i);
-        o[i].x = o[i].x * x + v.x * y;
-        o[i].y = o[i].y * x + v.y * y;
-        o[i].z = o[i].z * x + v.z * y;
-        o[i].w = o[i].w * x + v.w * y;
+        for (int k = 0; k < 4; ++k) {
+          const float *r = at(k0 + k < n ? k0 + k : n - 1);
+          mk[k] = k0 + k < n ? ld(r + S::Maxima + hd) : -INFINITY;
+          lk[k] = ld(r + S::Totals + hd);
+#pragma unroll
+          for (int i = 0; i < ND; ++i) v[k][i] = ld4(r + hd * S::HeadStep + d0 + 64 * i);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (mk[k] == -INFINITY) continue;  // no token seen
+          const float M2 = fmaxf(M, mk[k]);
+          const float x = M == -INFINITY ? 0.0f : ex2(M - M2), y = ex2(mk[k] - M2);
+          L = L * x + lk[k] * y;
+#pragma unroll
+          for (int i = 0; i < ND; ++i) {
+            o[i].x = o[i].x * x + v[k][i].x * y;
+            o[i].y = o[i].y * x + v[k][i].y * y;
+            o[i].z = o[i].z * x + v[k][i].z * y;
+            o[i].w = o[i].w * x + v[k][i].w * y;
+          }
+          M = M2;
+        }
       }
-      M = M2;
     };
     auto finish = [&] {
       if (hd >= nh) return;
@@ -585,10 +611,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
                    64 * i,
                a.o.dtype, make_float4(o[i].x * r, o[i].y * r, o[i].z * r, o[i].w * r));
     };
-    reset();
-    for (int k = 0; k < kWarps; ++k)
-      add(results + k * S::Slot, [](const float *p) { return *p; },
-          [](const float *p) { return *reinterpret_cast<const float4 *>(p); });
+    join(kWarps, [&](int64_t k) { return results + k * S::Slot; }, [](const float *p) { return *p; },
+         [](const float *p) { return *reinterpret_cast<const float4 *>(p); });
     const int64_t first = pre[this_b] * heads + int64_t(this_pass) * this_units;
     const int64_t last = first + this_units - 1;  // units of this pass
     if (first >= begin && last < end) {
@@ -598,10 +622,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
       const int64_t x0 = ((first + 1) * parts - 1) / total, x1 = ((last + 1) * parts - 1) / total;
       float *slot = a.partials + (blockIdx.x * 2 + (cur == begin ? 0 : 1)) * int64_t(S::Slot);
 #pragma unroll
-      for (int i = 0; i < ND; ++i) *reinterpret_cast<float4 *>(slot + hd * D + d0 + 64 * i) = o[i];
+      for (int i = 0; i < ND; ++i) *reinterpret_cast<float4 *>(slot + hd * S::HeadStep + d0 + 64 * i) = o[i];
       if ((tid & 15) == 0) {
-        slot[kHeads * D + hd] = M;
-        slot[kHeads * D + kHeads + hd] = L;
+        slot[S::Maxima + hd] = M;
+        slot[S::Totals + hd] = L;
       }
       __threadfence();
       __syncthreads();
@@ -614,11 +638,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         // Part x0 has this pass as its last segment (slot 1) unless it begins with it; the others
         // begin with it. Parts follow one another in the workspace two slots apart.
         const int64_t begin0 = x0 * total / parts;
-        reset();
-        for (int64_t x = x0; x <= x1; ++x)
-          add(a.partials + (x * 2 + (x == x0 && begin0 < first ? 1 : 0)) * int64_t(S::Slot),
-              [](const float *p) { return __ldcg(p); },
-              [](const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); });
+        join(x1 - x0 + 1,
+             [&](int64_t k) {
+               return a.partials + ((x0 + k) * 2 + (k == 0 && begin0 < first ? 1 : 0)) * int64_t(S::Slot);
+             },
+             [](const float *p) { return __ldcg(p); },
+             [](const float *p) { return __ldcg(reinterpret_cast<const float4 *>(p)); });
         finish();
       }
     }
