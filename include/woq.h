@@ -339,8 +339,8 @@ int qgemm_bf16_noalloc(const float *X, int64_t m, const woq_weight *w, float *Y,
 /*
  * Rows of heads in device memory: element (t, h, d) is at data + t * row_stride +
  * h * head_stride + d, strides in elements. A slice of a fused projection's output [t, q | k | v]
- * is such an array. data is 16-byte aligned and both strides are positive multiples of 16 bytes;
- * head_stride is at least the heads' dim.
+ * is such an array. data is 16-byte aligned (NULL for no rows) and both strides are positive multiples
+ * of 16 bytes; head_stride is at least the heads' dim.
  */
 typedef struct woq_rows {
   void *data;
@@ -394,7 +394,7 @@ int kv4_append(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64
  * kv4_gather -- reads rows of the cache back, scale * code, addressed as kv4_append addresses them
  * (a float32 result is exact; 16-bit ones are rounded once). A row of a sequence whose token has no
  * page becomes 0; rows outside the sequences are left as they are. Arguments and errors as
- * kv4_append, with k and v written.
+ * kv4_append, with k and v written, and WOQ_EINVAL where they share bytes.
  */
 int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, int32_t batch, const int32_t *table,
                int64_t width, int64_t tokens, const woq_rows *k, const woq_rows *v, void *stream);
@@ -416,7 +416,7 @@ int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, in
  * sums. 16-bit: operands as they are, weights rounded to the type. The lengths stay on the device; the grid
  * goes by tokens and batch. Deterministic. A value that is not finite enters only rows that see it: a
  * row that sees such a q or k is NaN, one that sees such a v is not finite in its column.
- * batch 1 to 2^20; (tokens / 256 + batch) * q.heads < 2^31.
+ * batch 1 to 2^20; (tokens / 256 + batch) * q.heads < 2^31; tokens == 0 does nothing.
  * Errors: WOQ_EINVAL (null pointers, dtypes, heads, batch, scale, overlap), WOQ_ESHAPE (dim, sizes, strides),
  * WOQ_EALIGN, WOQ_EWORKSPACE, WOQ_EDEVICE, WOQ_ECUDA. Waits inside the kernel are bounded, as qgemm's.
  */

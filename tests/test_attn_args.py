@@ -149,3 +149,37 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
             call()
     for name in ("attn_prompt", "kv4_append", "kv4_gather", "kv4_attn", "KV4Cache"):
         assert name in woq.__all__
+
+
+def test_no_rows_and_interleaved_arrays():
+    """Empty prompts have no address; arrays that only interleave are not refused. Without a device both end there."""
+    L = _lib.lib()
+    through = (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE)
+    none = _lib.WOQ_OK if torch.cuda.is_available() else None
+    c, r, big = kv4(), rows(data=0), rows(data=0, heads=4, row=512)
+    for rc in (L.kv4_append(ctypes.byref(c), ctypes.byref(r), ctypes.byref(r), 0, OK, None, 1, OK, 1, None),
+               L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, 0, ctypes.byref(r), ctypes.byref(r), None),
+               L.attn_prompt(ctypes.byref(big), ctypes.byref(r), ctypes.byref(r), 0, OK, 1, 128, 0.1, ctypes.byref(big),
+                             None, 0, None)):
+        assert rc in through or rc == none
+
+    def gather(a, b, tokens=4):
+        return L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, tokens, ctypes.byref(a), ctypes.byref(b), None)
+
+    if not torch.cuda.is_available():  # these would run
+        size = 4
+        for a, b in (
+            (rows(row=512, head=256), rows(data=OK + 128 * size, row=512, head=256)),  # [tokens, heads, 2, dim]
+            (rows(data=OK + 128 * size, row=512, head=256), rows(row=512, head=256)),
+            (rows(row=512), rows(data=OK + 256 * size, row=512)),  # [tokens, 2, heads, dim]
+            (rows(row=128, head=1024), rows(data=OK + 512 * size, row=128, head=1024)),  # [heads, 2, tokens, dim]
+            (rows(row=256, head=1024), rows(data=OK + 128 * size, row=256, head=1024)),  # [heads, tokens, 2, dim]
+        ):
+            assert gather(a, b) in through
+    for a, b in (
+        (rows(row=512, head=256), rows(data=OK + 256 * 4, row=512, head=256)),  # on the other head
+        (rows(row=128, head=1024), rows(data=OK + 384 * 4, row=128, head=1024)),  # on the last token
+        (rows(row=256, head=1024), rows(data=OK + 256 * 4, row=256, head=1024)),  # on the next token
+        (rows(row=768, head=256), rows(data=OK + 64 * 4, row=768, head=256)),  # half a row
+    ):
+        assert gather(a, b) == gather(b, a) == _lib.WOQ_EINVAL

@@ -1,6 +1,8 @@
 """The 4-bit cache: kv4_append and kv4_gather against the oracle's quantiser, bit for bit, and kv4_attn against
 attention in 64 bits over the values that the cache holds."""
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -332,3 +334,21 @@ def test_two_workspaces_on_two_streams():
             for s, w in zip(streams, spaces)]
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for row in outs for o in row)
+
+
+def test_no_tokens_and_interleaved_results():
+    """Calls with no rows, a cache that is copied, and k and v gathered into one array [tokens, heads, 2, dim]."""
+    torch.manual_seed(5)
+    cache, cu, table = woq.KV4Cache.empty(3, 2, 64, 16), ints([0, 40]), ints([[2, 0, 1]])
+    x = torch.randn(40, 2, 64, device="cuda")
+    woq.kv4_append(cache, x, -x, cu, table)
+    empty = torch.empty(0, 2, 64, device="cuda")
+    before = cache.codes.clone()
+    woq.kv4_append(cache, empty, empty, ints([0, 0]), table)
+    k, v = woq.kv4_gather(cache, ints([0, 0]), table, tokens=0)
+    assert k.shape == v.shape == empty.shape and torch.equal(cache.codes, before)
+    assert woq.attn_prompt(empty, empty, empty, ints([0, 0])).shape == empty.shape
+    k, v = woq.kv4_gather(cache, cu, table, tokens=40)
+    both = torch.empty(40, 2, 2, 64, device="cuda")
+    woq.kv4_gather(copy.deepcopy(cache), cu, table, k_out=both[:, :, 0], v_out=both[:, :, 1])
+    assert torch.equal(both[:, :, 0], k) and torch.equal(both[:, :, 1], v) and torch.equal(v, -k)

@@ -304,6 +304,7 @@ def _device_of(t: torch.Tensor, what: str) -> int:
     return d
 
 
+# Structures are handed over as they are, by reference: a byref() for each costs a tenth of a call.
 def _rows(t: torch.Tensor, what: str, device: int) -> _lib.WoqRows:
     """The [rows, heads, dim] tensor ``t`` as the C ABI takes it; dim contiguous."""
     dtype, shape, stride = _DTYPES.get(t.dtype), t.shape, t.stride()
@@ -377,8 +378,8 @@ def attn_prompt(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu: torch.Ten
         with torch.cuda.stream(stream):
             workspace = attn_prompt_workspace(q, k, batch)
     ws, nbytes = _space(workspace, d)
-    rc = _lib.lib().attn_prompt(ctypes.byref(qr), ctypes.byref(kr), ctypes.byref(vr), tokens, cp, batch, dim,
-                                dim**-0.5 if scale is None else scale, ctypes.byref(orow), ws, nbytes,
+    rc = _lib.lib().attn_prompt(qr, kr, vr, tokens, cp, batch, dim,
+                                dim**-0.5 if scale is None else scale, orow, ws, nbytes,
                                 _raw_stream(stream, d))
     if rc:
         _lib.check(rc, "attn_prompt")
@@ -405,10 +406,13 @@ class KV4Cache:
             raise ValueError("scales must be a contiguous float16 tensor [pages, kv_heads, page, 2, dim / 32]")
         if c.device != s.device:
             raise ValueError("codes and scales must be on one device")
+        object.__setattr__(self, "pages", pages)
         object.__setattr__(self, "kv_heads", heads)
         object.__setattr__(self, "dim", 2 * half)
         object.__setattr__(self, "page", page)
-        object.__setattr__(self, "_desc", _lib.WoqKv4(_ptr(c), _ptr(s), pages, heads, 2 * half, page))
+
+    def desc(self) -> _lib.WoqKv4:
+        return _lib.WoqKv4(self.codes.data_ptr(), self.scales.data_ptr(), self.pages, self.kv_heads, self.dim, self.page)
 
     @classmethod
     def empty(cls, pages: int, kv_heads: int, dim: int, page: int = 64, device="cuda") -> "KV4Cache":
@@ -422,9 +426,10 @@ class KV4Cache:
     def nbytes(self) -> int:
         return self.codes.numel() + 2 * self.scales.numel()
 
+
 def _step_args(cache, k, v, cu, table, start, what):
     d = _device_of(cache.codes, "the cache")
-    c = ctypes.byref(cache._desc)
+    c = cache.desc()
     kr, vr = _rows(k, "k", d), _rows(v, "v", d)
     shape = k.shape
     if shape != v.shape or shape[1] != cache.kv_heads or shape[2] != cache.dim:
@@ -444,7 +449,7 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, cu: torch.Tens
     (C ABI ``kv4_append``). Rows cu[b] .. cu[b + 1] - 1 become tokens start[b], start[b] + 1, ... of
     sequence b, whose pages are table[b]; ``start`` None: each sequence is new."""
     d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k, v, cu, table, start, "kv4_append")
-    rc = _lib.lib().kv4_append(c, ctypes.byref(kr), ctypes.byref(vr), k.shape[0], cp, sp, batch, tp, width,
+    rc = _lib.lib().kv4_append(c, kr, vr, k.shape[0], cp, sp, batch, tp, width,
                                _raw_stream(stream, d))
     if rc:
         _lib.check(rc, "kv4_append")
@@ -463,7 +468,7 @@ def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: to
         with torch.cuda.stream(stream):
             k_out, v_out = (torch.zeros(shape, dtype=dtype, device=cache.codes.device) for _ in "kv")
     d, c, kr, vr, cp, sp, batch, tp, width = _step_args(cache, k_out, v_out, cu, table, start, "kv4_gather")
-    rc = _lib.lib().kv4_gather(c, cp, sp, batch, tp, width, k_out.shape[0], ctypes.byref(kr), ctypes.byref(vr),
+    rc = _lib.lib().kv4_gather(c, cp, sp, batch, tp, width, k_out.shape[0], kr, vr,
                                _raw_stream(stream, d))
     if rc:
         _lib.check(rc, "kv4_gather")
@@ -473,7 +478,7 @@ def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: to
 def kv4_attn_workspace(cache: KV4Cache, q: torch.Tensor) -> torch.Tensor:
     """A zeroed workspace for kv4_attn calls with queries shaped like ``q`` (every call leaves its
     counters zero; calls that share one must be ordered on one stream)."""
-    need = _lib.lib().kv4_attn_workspace_bytes(ctypes.byref(cache._desc), q.shape[1], q.shape[0])
+    need = _lib.lib().kv4_attn_workspace_bytes(cache.desc(), q.shape[1], q.shape[0])
     return torch.zeros(int(need), dtype=torch.uint8, device=cache.codes.device)
 
 
@@ -485,7 +490,8 @@ def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.
     d = _device_of(cache.codes, "the cache")
     qr = _rows(q, "q", d)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        with torch.cuda.stream(stream):
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     orow = _rows(out, "out", d)
     lp, tp = _ints(lens, "lens", 1, d), _ints(table, "table", 2, d)
     batch, width = table.shape
@@ -497,8 +503,9 @@ def kv4_attn(q: torch.Tensor, cache: KV4Cache, lens: torch.Tensor, table: torch.
         with torch.cuda.stream(stream):
             workspace = kv4_attn_workspace(cache, q)
     ws, nbytes = _space(workspace, d)
-    rc = _lib.lib().kv4_attn(ctypes.byref(qr), ctypes.byref(cache._desc), lp, batch, tp, width, cache.dim**-0.5 if scale is None else scale,
-                             ctypes.byref(orow), ws, nbytes, _raw_stream(stream, d))
+    rc = _lib.lib().kv4_attn(qr, cache.desc(), lp, batch, tp, width,
+                             cache.dim**-0.5 if scale is None else scale, orow, ws, nbytes,
+                             _raw_stream(stream, d))
     if rc:
         _lib.check(rc, "kv4_attn")
     return out

@@ -1,5 +1,6 @@
 // C-ABI entry points of the attention calls (declared in include/woq.h): argument checks, the
 // device check and dispatch to the kernel launchers. Nothing here allocates or synchronises.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 
@@ -16,8 +17,8 @@ bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int64_t size_of(int32_t dtype) { return dtype == WOQ_F32 ? 4 : 2; }
 
-int check_rows(const woq_rows *r, int64_t heads, int64_t dim) {
-  if (!r || !r->data) return WOQ_EINVAL;
+int check_rows(const woq_rows *r, int64_t rows, int64_t heads, int64_t dim) {
+  if (!r || (rows > 0 && !r->data)) return WOQ_EINVAL;
   if (r->dtype != WOQ_F32 && r->dtype != WOQ_F16 && r->dtype != WOQ_BF16) return WOQ_EINVAL;
   if (r->heads != heads) return WOQ_EINVAL;
   const int64_t unit = 16 / size_of(r->dtype);
@@ -52,19 +53,27 @@ Span span(const woq_rows &r, int64_t rows, int64_t dim) {
   return {p, p + static_cast<uintptr_t>(last * size_of(r.dtype))};
 }
 
-// Whether an output shares bytes with an input. Slices of one fused array interleave without
-// sharing: with equal strides, rows apart by less than a row are compared within one row.
+// Whether an output shares bytes with another array. Slices of one fused array interleave without sharing
+// any: they are compared within one row of all heads, within one head of all rows, and within one row of a
+// head, wherever both arrays repeat at the same distance.
 bool overlap(const woq_rows &a, const woq_rows &b, int64_t rows, int64_t dim) {
   const Span x = span(a, rows, dim), y = span(b, rows, dim);
   if (x.last <= y.first || y.last <= x.first) return false;
   const int64_t size = size_of(a.dtype);
-  const uintptr_t pitch = static_cast<uintptr_t>(a.row_stride * size);
-  if (size != size_of(b.dtype) || a.row_stride != b.row_stride) return true;
-  const uintptr_t in_a = static_cast<uintptr_t>(((a.heads - 1) * a.head_stride + dim) * size);
-  const uintptr_t in_b = static_cast<uintptr_t>(((b.heads - 1) * b.head_stride + dim) * size);
-  const uintptr_t d = x.first <= y.first ? (y.first - x.first) % pitch : pitch - (x.first - y.first) % pitch;
-  // b's row starts d bytes into a row of a: apart if it begins behind a's heads and ends before the next row
-  return !(d % pitch >= in_a && d % pitch + in_b <= pitch);
+  if (size != size_of(b.dtype)) return true;
+  // b starts d bytes into a period of a: apart if that is behind a's bytes and b's end before the next period
+  auto apart = [&](int64_t period, int64_t in_a, int64_t in_b) {
+    const uintptr_t p = static_cast<uintptr_t>(period * size);
+    const uintptr_t d = x.first <= y.first ? (y.first - x.first) % p : p - (x.first - y.first) % p;
+    return d % p >= static_cast<uintptr_t>(in_a * size) && d % p + static_cast<uintptr_t>(in_b * size) <= p;
+  };
+  const int64_t row = a.row_stride, head = a.head_stride;
+  const bool same_rows = row == b.row_stride, same_heads = head == b.head_stride;
+  if (same_rows && apart(row, (a.heads - 1) * head + dim, (b.heads - 1) * b.head_stride + dim)) return false;
+  if (same_heads && apart(head, (rows - 1) * row + dim, (rows - 1) * b.row_stride + dim)) return false;
+  if (same_rows && same_heads && (row % head == 0 || head % row == 0) && apart(std::min(row, head), dim, dim))
+    return false;
+  return true;
 }
 
 int check_step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
@@ -76,8 +85,8 @@ int check_step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64
   if (!cu || tokens < 0) return WOQ_EINVAL;
   if (tokens > INT32_MAX) return WOQ_ESHAPE;
   if (!aligned(cu, 4) || !aligned(start, 4)) return WOQ_EALIGN;
-  rc = check_rows(k, cache->kv_heads, cache->dim);
-  return rc != WOQ_OK ? rc : check_rows(v, cache->kv_heads, cache->dim);
+  rc = check_rows(k, tokens, cache->kv_heads, cache->dim);
+  return rc != WOQ_OK ? rc : check_rows(v, tokens, cache->kv_heads, cache->dim);
 }
 
 int step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
@@ -126,9 +135,9 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
   if (rc != WOQ_OK) return rc;
   if (!q || !o || !lens) return WOQ_EINVAL;
   if (q->heads < 1 || q->heads % cache->kv_heads || q->heads / cache->kv_heads > woq::kMaxGroup) return WOQ_EINVAL;
-  rc = woq::check_rows(q, q->heads, cache->dim);
+  rc = woq::check_rows(q, batch, q->heads, cache->dim);
   if (rc != WOQ_OK) return rc;
-  rc = woq::check_rows(o, q->heads, cache->dim);
+  rc = woq::check_rows(o, batch, q->heads, cache->dim);
   if (rc != WOQ_OK) return rc;
   if (o->dtype != q->dtype || !(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
   if (!woq::aligned(lens, 4)) return WOQ_EALIGN;
@@ -163,7 +172,7 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
   if (!prompt_heads(q->heads, k->heads)) return WOQ_EINVAL;
   const woq_rows *all[4] = {q, k, v, o};
   for (int i = 0; i < 4; ++i) {
-    const int rc = woq::check_rows(all[i], i == 0 || i == 3 ? q->heads : k->heads, dim);
+    const int rc = woq::check_rows(all[i], tokens, i == 0 || i == 3 ? q->heads : k->heads, dim);
     if (rc != WOQ_OK) return rc;
     if (all[i]->dtype != q->dtype) return WOQ_EINVAL;
   }
