@@ -96,8 +96,9 @@ struct Shared {
   // [query tile][its scores' buffer]: 16-bit rows have one, float32 rows two. s_free, 16-bit rows: read by
   // the query tile's warps; float32 rows: the weights in their place have been multiplied.
   uint64_t s_full[2][2], s_free[2][2];
-  // Weights written; with float32 rows also the product before it read out, which has the place of the next.
-  uint64_t p_full[2];
+  // Weights written; with float32 rows also the product before it read out, which has the place of the next. A
+  // warp may be a tile ahead of the others in its query tile, as its scores are: float32 rows have one for each buffer.
+  uint64_t p_full[2][2];
   uint64_t t_full[2];
   uint64_t look[kBlockRows / 64 + 1];    // the copy of a diagonal tile's values is under way
   uint64_t looked[kBlockRows / 64 + 1];  // they are there, and finite
@@ -257,8 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int b = 0; b < 2; ++b) {
         ptx::mbar_init(&sh.s_full[i][b], 1);
         ptx::mbar_init(&sh.s_free[i][b], MODE == kSplit ? 1 : 4);
+        ptx::mbar_init(&sh.p_full[i][b], MODE == kSplit ? 8 : 4);
       }
-      ptx::mbar_init(&sh.p_full[i], MODE == kSplit ? 8 : 4);
       ptx::mbar_init(&sh.t_full[i], 1);
     }
     for (int i = 0; i < ST; ++i) {
@@ -441,7 +442,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int t = 0; t < 2; ++t) {
               if (j >= (t ? n1 : n0)) continue;
-              if (!wait(&sh.p_full[t], j & 1)) break;
+              if (!wait(&sh.p_full[t][MODE == kSplit ? j & 1 : 0], (MODE == kSplit ? j >> 1 : j) & 1)) break;
               ptx::tc_fence_after();
               values(t, j, t == 1 || j >= n1);
             }
@@ -622,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);
       }
       if (ok && n > 0) wait(&sh.t_full[t], (n - 1) & 1);
       if (ok && n > 0) wait(&sh.looked_all, 0);
@@ -674,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(j + 1) & 1]);
       };
       // A tile's weights come before the tile before it is added, whose factors are kept until then.
 #pragma unroll 1
@@ -750,9 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);
+        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][j & 1]);
         if (j > 0) accumulate(j - 1, alpha_last, v_pow);
-        else if (lane == 0) ptx::mbar_arrive(&sh.p_full[t]);  // nothing to read out yet
+        else if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);  // nothing to read out yet
         v_pow = v_next;
       }
       if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
