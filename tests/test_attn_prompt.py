@@ -239,3 +239,27 @@ def test_a_stuck_wait_gives_up_and_the_context_survives():
         L.woq_debug_set_wait_limit(0)
     assert torch.equal(woq.attn_prompt(q, k, v, ints([0, 300])), want)
     assert woq.device_status(clear=True) == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("dim", [64, 128])
+def test_many_more_tiles_than_blocks_run_at_once(dtype, dim):
+    """A block goes on from tile to tile: sequences of one to a few tiles of rows, some empty, some with values that
+    are not finite, and the same bits on every call."""
+    lens = [300, 1, 0, 513, 64, 900, 257, 5, 0, 1100, 128, 256, 129, 31] * 3
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    q, k, v = fused(14, cu[-1], 24, 8, dim, dtype)
+    out = check(q, k, v, cu)
+    for _ in range(3):
+        assert torch.equal(woq.attn_prompt(q, k, v, ints(cu)), out)
+    v2 = v.clone()
+    hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+    for i in range(0, len(lens), 3):  # the last value of every third sequence
+        if lens[i]:
+            v2[cu[i + 1] - 1, 3, 17] = float("inf")
+            hit[cu[i + 1] - 1, 9:12, 17] = True
+    got = woq.attn_prompt(q, k, v2, ints(cu))
+    assert torch.equal(~got.isfinite(), hit)
+    if dtype != torch.float32:  # float32: such a value has no part in its tile's power of two
+        assert torch.equal(got[~hit], out[~hit])
+    assert woq.device_status() == _lib.WOQ_OK

@@ -12,6 +12,12 @@
 // warps 8 has the copies (TMA), 9 issues the scores' matrix instructions, 10 the values', and 11 looks at the
 // values on the diagonal. Longest rows come first in a sequence, so that a launch ends with its shortest blocks.
 //
+// A block that has asked for the last of its copies takes over a block that has not started (cluster launch control):
+// that one's place is looked up and its keys, values and, 16-bit rows, queries are under way while the last tiles
+// of this one and its output are worked on. Barriers count on from item to item. Against a launch for each block:
+// 16 bfloat16 prompts of 301 to 4003 tokens 969 -> 896 us, 3 binary16 ones of 1 to 5003 at dim 64 99 -> 88, 32,768
+// bfloat16 tokens 4.01 -> 3.85 ms, 4096 float32 ones 243 -> 238 us; 137 float32 ones, one item a block, 20.2 -> 20.5.
+//
 // 16-bit rows: the output is summed in tensor memory, against a maximum that may lag behind (at the loop). float32
 // rows: each tile's product starts from zero and is added to the output in registers, so that sums
 // inside the tensor cores, which cut off instead of rounding, run over BK keys at most; scores are one tile ahead.
@@ -24,12 +30,12 @@
 // block has the SM, and nothing runs under it.
 //
 // Masked weights are exact zeros, but zero times a value that is not finite is NaN. The tiles on the diagonal hold
-// every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory, and
-// added after the last tile to the rows that do see it.
+// every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory,
+// and added after the last tile to the rows that do see it.
 //
-// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20 us, 4096 209 us (28 of them the
-// planes; 1.14 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 708 us (146 the planes); 32,768 bfloat16
-// tokens 4.05 ms, 1.09 PFLOP/s, at the clock that the power cap leaves.
+// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20.5 us, 4096 238 us (28 of them the
+// planes; 0.98 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 718 us (146 the planes); 32,768 bfloat16
+// tokens 3.85 ms, 1.14 PFLOP/s, at the clock that the power cap leaves.
 #include <algorithm>
 #include <mutex>
 
@@ -63,7 +69,9 @@ struct Cfg {
   static constexpr int Subs = D / 64;                        // 128-byte columns of a tile
   static constexpr int QBytes = Parts * kRows * D * 2;
   static constexpr int KvBytes = Parts * BK * D * 2;
-  static constexpr int Room = 227 * 1024 - 2048 - 2 * QBytes;
+  // A 16-bit block has its next queries on the way while it still needs these; float32 queries fill the room.
+  static constexpr int QBufs = MODE == kSplit ? 1 : 2;
+  static constexpr int Room = 227 * 1024 - 2048 - QBufs * 2 * QBytes;
   static constexpr int Stages = Room / KvBytes > 6 ? 6 : Room / KvBytes;
   static_assert(MODE != kSplit || BK == kSplitRows, "one power of two a tile");
   static_assert(Stages >= 3, "keys and values of two tiles are in flight at once");
@@ -71,7 +79,7 @@ struct Cfg {
   // warps that issue matrix instructions must not spill: they set the pace.
   static constexpr int QueryRegs = MODE == kSplit ? 216 : 200, HelperRegs = MODE == kSplit ? 72 : 104;
   static_assert(256 * QueryRegs + 128 * HelperRegs <= kThreads * kLaunchRegs, "register split");
-  static constexpr int Smem = 2 * QBytes + Stages * KvBytes + 2048;
+  static constexpr int Smem = QBufs * 2 * QBytes + Stages * KvBytes + 2048;
 };
 
 struct Maps {
@@ -90,8 +98,19 @@ struct Args {
   long long wait_limit, stuck_wait;
 };
 
+constexpr int kLooks = kBlockRows / 64 + 1;  // at least the tiles on a block's diagonal
+
+// The tile of query rows that a block has in hand; the next one's record is written beside it.
+struct Item {
+  int head, start, len, r0, tile0;  // len 0: there are no more
+};
+
 struct Shared {
-  uint64_t q_full[2];
+  uint4 claim;        // the answer to a claim of another block's tile
+  uint64_t claimed;
+  uint64_t item_full[2];
+  uint64_t done[2];   // [item & 1] the query warps have written the item's rows
+  uint64_t q_full[2][2];  // [buffer][query tile]
   uint64_t kv_full[8], kv_empty[8];
   // [query tile][its scores' buffer]: 16-bit rows have one, float32 rows two. s_free, 16-bit rows: read by
   // the query tile's warps; float32 rows: the weights in their place have been multiplied.
@@ -100,14 +119,14 @@ struct Shared {
   // warp may be a tile ahead of the others in its query tile, as its scores are: float32 rows have one for each buffer.
   uint64_t p_full[2][2];
   uint64_t t_full[2];
-  uint64_t look[kBlockRows / 64 + 1];    // the copy of a diagonal tile's values is under way
-  uint64_t looked[kBlockRows / 64 + 1];  // they are there, and finite
+  uint64_t look[kLooks];    // the copy of a diagonal tile's values is under way
+  uint64_t looked[kLooks];  // they are there, and finite
   uint64_t looked_all;
   uint64_t drain, never;
+  Item item[2];
   uint32_t tmem;
   int abort;
-  int nonfinite;
-  int b, r0, start, len, tile0;  // the block's rows
+  int nonfinite[2];  // [item & 1]
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
-  uint8_t *smem_kv = smem + 2 * C::QBytes;
+  uint8_t *smem_kv = smem + C::QBufs * 2 * C::QBytes;
   Shared &sh = *reinterpret_cast<Shared *>(smem_kv + ST * C::KvBytes);
   volatile int *abort = &sh.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -253,8 +272,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::tmem_relinquish();
   }
   if (warp == 1 && lane == 0) {
+    ptx::mbar_init(&sh.claimed, 1);
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(&sh.q_full[i], 1);
+      ptx::mbar_init(&sh.item_full[i], 1);
+      ptx::mbar_init(&sh.done[i], 8);
+      for (int b = 0; b < 2; ++b) ptx::mbar_init(&sh.q_full[i][b], 1);
       for (int b = 0; b < 2; ++b) {
         ptx::mbar_init(&sh.s_full[i][b], 1);
         ptx::mbar_init(&sh.s_free[i][b], MODE == kSplit ? 1 : 4);
@@ -266,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ptx::mbar_init(&sh.kv_full[i], 1);
       ptx::mbar_init(&sh.kv_empty[i], 1);
     }
-    for (int i = 0; i <= kBlockRows / 64; ++i) {
+    for (int i = 0; i < kLooks; ++i) {
       ptx::mbar_init(&sh.look[i], 1);
       ptx::mbar_init(&sh.looked[i], 1);
     }
@@ -274,83 +296,143 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::mbar_init(&sh.drain, 2);
     ptx::mbar_init(&sh.never, 1);
     ptx::fence_mbar_init();
+    sh.abort = 0;
   }
   ptx::pdl_wait();
-  const int head = static_cast<int>(blockIdx.x % a.q_heads);
-  if (warp == 0) {
-    Place p{};
-    const bool found = find_tile(a.cu, a.batch, a.tokens, blockIdx.x / a.q_heads, kBlockRows, p);
-    if (lane == 0) {
-      sh.len = found ? p.len : 0;
-      sh.start = p.start;
-      sh.r0 = found ? (p.tiles - 1 - p.tile) * kBlockRows : 0;  // a sequence's longest rows first
-      sh.tile0 = p.split0;
-      sh.abort = 0;
-      sh.nonfinite = 0;
-    }
-  }
+  Place place{};
+  bool found = false;  // warp 8's: the item that it is about to hand out
+  if (warp == 8) found = find_tile(a.cu, a.batch, a.tokens, blockIdx.x / a.q_heads, kBlockRows, place);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
-  const int len = sh.len, r0 = sh.r0, start = sh.start;
   const uint32_t tmem = sh.tmem;
-  if (len == 0) {  // fewer tiles than blocks
-    ptx::pdl_launch_dependents();
-    if (warp == 9) ptx::tmem_dealloc(tmem, kTmemCols);
-    return;
-  }
 
-  // Key tiles of the two query tiles: up to the diagonal, and not behind the last row.
-  auto tiles_of = [&](int t) {
-    const int first = r0 + t * kRows;
-    const int rows = min(len, first + kRows);
-    return first < len ? (rows + BK - 1) / BK : 0;
+  // An item's key tiles: up to the diagonal, and not behind the last row.
+  struct Work {
+    int head, start, len, r0;
+    int n0, n1, nt, diag;  // tiles of the two query tiles, of both, and the first with masked pairs
   };
-  const int n0 = tiles_of(0), n1 = tiles_of(1);
-  const int nt = max(n0, n1);
-  const int diag = r0 / BK;  // the first tile with masked pairs
-  const int kv_head = head / a.group;
-
-  int issued = 0;  // copies' slots filled so far
-  // The ring's slots in order: k 0, k 1, v 0, k 2, v 1, ...
-  auto k_slot = [](int j) { return j > 0 ? 2 * j - 1 : 0; };
-  auto v_slot = [nt](int j) { return j + 1 < nt ? 2 * j + 2 : 2 * j + 1; };
+  auto read_item = [&](int it) {
+    const Item &i = sh.item[it & 1];
+    Work w{i.head, i.start, i.len, i.r0, 0, 0, 0, 0};
+    w.n0 = (min(w.len, w.r0 + kRows) + BK - 1) / BK;
+    w.n1 = w.r0 + kRows < w.len ? (min(w.len, w.r0 + 2 * kRows) + BK - 1) / BK : 0;
+    w.nt = max(w.n0, w.n1);
+    w.diag = w.r0 / BK;
+    return w;
+  };
+  // Barriers count on from item to item. The ring's slots in order: k 0, k 1, v 0, k 2, v 1, ... of an item; `ring`
+  // is its first one's place, modulo two rounds, and `looks` likewise its first diagonal tile's.
+  int ring = 0, looks = 0;
+  auto k_slot = [&](int j) { return ring + (j > 0 ? 2 * j - 1 : 0); };
+  auto v_slot = [&](int j, int nt) { return ring + (j + 1 < nt ? 2 * j + 2 : 2 * j + 1); };
+  auto advance = [&](const Work &w) {
+    ring = (ring + 2 * w.nt) % (2 * ST);
+    looks = (looks + w.nt - w.diag) % (2 * kLooks);
+  };
 
   if (warp >= 8) {
     ptx::regs_dec<C::HelperRegs>();
     if (warp == 8) {
-      // ---- copies, in the order in which the matrix instructions take them ----
-      if (lane == 0) {
-        auto query = [&](int t) {
-          ptx::mbar_arrive_expect_tx(&sh.q_full[t], C::QBytes);
-          for (int p = 0; p < C::Parts; ++p)
-            for (int c = 0; c < C::Subs; ++c)
-              ptx::tma_load_3d(smem + t * C::QBytes + (p * C::Subs + c) * kRows * 128, &maps.q[p], &sh.q_full[t],
-                               64 * c, head, start + r0 + t * kRows);
-        };
-        auto kv = [&](const CUtensorMap *m, int tile) {
-          const int slot = issued % ST;
-          if (!ptx::mbar_wait_bounded(&sh.kv_empty[slot], ((issued / ST) & 1) ^ 1, a.wait_limit, abort)) {
-            record_timeout(abort);
-            return false;
-          }
-          ptx::mbar_arrive_expect_tx(&sh.kv_full[slot], C::KvBytes);
-          for (int p = 0; p < C::Parts; ++p)
-            for (int c = 0; c < C::Subs; ++c)
-              ptx::tma_load_3d(smem_kv + slot * C::KvBytes + (p * C::Subs + c) * BK * 128, &m[p],
-                               &sh.kv_full[slot], 64 * c, kv_head, start + tile * BK);
-          ++issued;
-          return true;
-        };
-        query(0);
-        bool ok = kv(maps.k, 0);
-        if (n1 > 0) query(1);
-#pragma unroll 1
-        for (int j = 0; j < nt && ok; ++j) {
-          if (j + 1 < nt) ok = kv(maps.k, j + 1);
-          ok = ok && kv(maps.v, j);
-          if (ok && j >= diag) ptx::mbar_arrive(&sh.look[j - diag]);
+      // ---- items, and their copies in the order in which the matrix instructions take them ----
+      int64_t target = blockIdx.x;
+      long long issued = 0;  // slots filled so far
+      bool ok = true;
+      auto wait_lane = [&](uint64_t *bar, uint32_t parity) {
+        if (ok && !ptx::mbar_wait_bounded(bar, parity, a.wait_limit, abort)) {
+          record_timeout(abort);
+          ok = false;
         }
+        return ok;
+      };
+      int it = 0, claims = 0, loaded = 0;  // items, claims, items whose queries were copied
+      for (;;) {
+        if (found || target < 0) {
+          ok = it < 2 || warp_wait(&sh.done[it & 1], (it - 2) >> 1 & 1, a.wait_limit, abort);
+          if (!ok) {
+            record_timeout(abort);
+            break;
+          }
+          if (lane == 0) {
+            // a sequence's longest rows first
+            sh.item[it & 1] = Item{static_cast<int>(target % a.q_heads), place.start, found ? place.len : 0,
+                                   (place.tiles - 1 - place.tile) * kBlockRows, place.split0};
+            ptx::mbar_arrive(&sh.item_full[it & 1]);
+          }
+          __syncwarp();
+        }
+        if (target < 0) break;
+        if (found && lane == 0) {
+          const Work w = read_item(it);
+          const int kv_head = w.head / a.group;
+          const int buf = it % C::QBufs;
+          auto queries = [&] {
+            for (int t = 0; t < 2; ++t) {
+              if (t == 1 && w.n1 == 0) {
+                ptx::mbar_arrive(&sh.q_full[buf][1]);  // so that its phases are the items'
+                break;
+              }
+              ptx::mbar_arrive_expect_tx(&sh.q_full[buf][t], C::QBytes);
+              for (int p = 0; p < C::Parts; ++p)
+                for (int c = 0; c < C::Subs; ++c)
+                  ptx::tma_load_3d(smem + (2 * buf + t) * C::QBytes + (p * C::Subs + c) * kRows * 128, &maps.q[p],
+                                   &sh.q_full[buf][t], 64 * c, w.head, w.start + w.r0 + t * kRows);
+            }
+            loaded = it + 1;
+          };
+          auto kv = [&](const CUtensorMap *m, int at, int tile) {
+            const int slot = at % ST;
+            if (!wait_lane(&sh.kv_empty[slot], ((at / ST) & 1) ^ 1)) return false;
+            ptx::mbar_arrive_expect_tx(&sh.kv_full[slot], C::KvBytes);
+            for (int p = 0; p < C::Parts; ++p)
+              for (int c = 0; c < C::Subs; ++c)
+                ptx::tma_load_3d(smem_kv + slot * C::KvBytes + (p * C::Subs + c) * BK * 128, &m[p],
+                                 &sh.kv_full[slot], 64 * c, kv_head, w.start + tile * BK);
+            ++issued;
+            return true;
+          };
+          const bool queries_first = C::QBufs == 2 || it == 0;
+          if (queries_first) queries();
+          kv(maps.k, k_slot(0), 0);
+#pragma unroll 1
+          for (int j = 0; j < w.nt && ok; ++j) {
+            if (j + 1 < w.nt) kv(maps.k, k_slot(j + 1), j + 1);
+            if (ok) kv(maps.v, v_slot(j, w.nt), j);
+            if (ok && j >= w.diag) ptx::mbar_arrive(&sh.look[(looks + j - w.diag) % kLooks]);
+            // their place is the last item's output's until that is written
+            if (ok && j == 0 && !queries_first && wait_lane(&sh.done[(it - 1) & 1], (it - 1) >> 1 & 1)) queries();
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (found) {
+          advance(read_item(it));
+          ++it;
+        }
+        if (!ok) break;
+        // The tile of a block that has not started yet: asked for only now, so that who is done first takes it.
+        if (lane == 0) {
+          ptx::fence_proxy_async_smem();
+          ptx::mbar_arrive_expect_tx(&sh.claimed, 16);
+          ptx::claim_block(&sh.claim, &sh.claimed);
+        }
+        int no_abort = 0;
+        if (!__all_sync(0xffffffffu, ptx::mbar_wait_bounded(&sh.claimed, claims++ & 1, kDrainLimit, &no_abort))) {
+          record_timeout(abort);
+          break;
+        }
+        uint32_t next;
+        target = ptx::claimed_block(&sh.claim, &next) ? static_cast<int64_t>(next) : -1;
+        found = target >= 0 && find_tile(a.cu, a.batch, a.tokens, target / a.q_heads, kBlockRows, place);
+        __syncwarp();
+      }
+      if (*abort && lane == 0) {
+        // What is in flight ends before the block does.
+        int no_abort = 0;
+        for (int i = max(0, loaded - C::QBufs); i < loaded; ++i)
+          for (int t = 0; t < 2; ++t)
+            ptx::mbar_wait_bounded(&sh.q_full[i % C::QBufs][t], i / C::QBufs & 1, kDrainLimit, &no_abort);
+        for (long long i = max(0LL, issued - ST); i < issued; ++i)
+          ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, kDrainLimit, &no_abort);
       }
     } else if (warp == 9 || warp == 10) {
       // ---- matrix instructions: the warp stays together, one lane issues. Warp 9 has the scores, warp 10 the
@@ -370,11 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (a.stuck_wait > 0) wait_for(&sh.never, 0, a.stuck_wait);  // test hook
         const uint32_t q_addr = ptx::smem_u32(smem), kv_addr = ptx::smem_u32(smem_kv);
         // Scores of tile j for the query tiles that it concerns, in one elected block: between two instructions
-        // the tensor cores wait for whatever the issuing thread does. `last`: the tile's keys are needed no more.
-        auto scores = [&](int j, bool first, bool second, bool last) {
-          const int b = MODE == kSplit ? j & 1 : 0;
-          const uint32_t d = uniform(tmem + b * BK);
-          const uint32_t q = uniform(desc_low(q_addr, 16));
+        // the tensor cores wait for whatever the issuing thread does.
+        // c0, c1: the query tiles' tiles before this one, of all items.
+        auto scores = [&](int j, int buf, int c0, int c1, bool first, bool second) {
+          const int b0 = MODE == kSplit ? c0 & 1 : 0, b1 = MODE == kSplit ? c1 & 1 : 0;
+          const uint32_t d0 = uniform(tmem + b0 * BK), d1 = uniform(tmem + kScores + b1 * BK);
+          const uint32_t q = uniform(desc_low(q_addr + buf * 2 * C::QBytes, 16));
           const uint32_t k = uniform(desc_low(kv_addr + k_slot(j) % ST * C::KvBytes, 16));
           if (ptx::elect_one()) {
 #pragma unroll
@@ -384,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)  // 16 elements are 2 units of 16 bytes
                   ptx::tc_mma_f16(
-                      d + t * kScores,
+                      t ? d1 : d0,
                       desc(q + (t * C::QBytes + pq * kPlaneQ + (kk >> 2) * kRows * 128) / 16 + (kk & 3) * 2),
                       desc(k + (pk * kPlaneK + (kk >> 2) * BK * 128) / 16 + (kk & 3) * 2), kIdescS, kk == 0 ? acc : 1);
               };
@@ -393,17 +476,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 product(0, 1, 1);
               }
               product(0, 0, MODE == kSplit);
-              ptx::tc_commit(&sh.s_full[t][b]);
+              ptx::tc_commit(&sh.s_full[t][t ? b1 : b0]);
             }
-            if (last) ptx::tc_commit(&sh.kv_empty[k_slot(j) % ST]);
+            ptx::tc_commit(&sh.kv_empty[k_slot(j) % ST]);  // its keys are needed no more
           }
         };
         // Weights times values. 16-bit rows: added to what is there, from the second tile on; float32 rows: from
         // zero. `last`: the tile's values are needed no more.
-        auto values = [&](int t, int j, bool last) {
+        auto values = [&](int t, int j, int c, int slot, bool last) {
           const uint32_t d = uniform(tmem + kTile + t * D);
-          const uint32_t p = uniform(tmem + t * kScores + (MODE == kSplit ? (j & 1) * BK : BK));
-          const uint32_t v = uniform(desc_low(kv_addr + v_slot(j) % ST * C::KvBytes, BK * 128));
+          const uint32_t p = uniform(tmem + t * kScores + (MODE == kSplit ? (c & 1) * BK : BK));
+          const uint32_t v = uniform(desc_low(kv_addr + slot * C::KvBytes, BK * 128));
           if (ptx::elect_one()) {
             auto product = [&](int pp, int pv, uint32_t acc) {
 #pragma unroll
@@ -417,36 +500,54 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             product(0, 0, MODE == kSplit ? 1 : j > 0);
             ptx::tc_commit(&sh.t_full[t]);
-            if (MODE == kSplit) ptx::tc_commit(&sh.s_free[t][j & 1]);
-            if (last) ptx::tc_commit(&sh.kv_empty[v_slot(j) % ST]);
+            if (MODE == kSplit) ptx::tc_commit(&sh.s_free[t][c & 1]);
+            if (last) ptx::tc_commit(&sh.kv_empty[slot]);
           }
         };
         auto full = [&](int i) { return wait(&sh.kv_full[i % ST], (i / ST) & 1); };
-        if (warp == 9) {
+        int c0 = 0, c1 = 0;
 #pragma unroll 1
-          for (int j = 0; j < nt && ok; ++j) {
-            const bool first = j < n0, second = j < n1;
-            // The place for the scores is free: tile j is the j-th (16-bit) or j / 2-th one there.
-            const int b = MODE == kSplit ? j & 1 : 0, parity = ((MODE == kSplit ? j >> 1 : j) & 1) ^ 1;
-            if (!full(k_slot(j)) || (first && !wait(&sh.s_free[0][b], parity)) ||
-                (second && !wait(&sh.s_free[1][b], parity)))
-              break;
-            if (j == 0 && !(wait(&sh.q_full[0], 0) && (!second || wait(&sh.q_full[1], 0)))) break;
-            ptx::tc_fence_after();
-            scores(j, first, second, true);
-          }
-        } else {
+        for (int it = 0; wait(&sh.item_full[it & 1], it >> 1 & 1); ++it) {
+          const Work w = read_item(it);
+          if (w.len == 0) break;
+          if (warp == 9) {
+            const int buf = it % C::QBufs;
 #pragma unroll 1
-          for (int j = 0; j < nt && ok; ++j) {
-            if (!full(v_slot(j)) || (j >= diag && !wait(&sh.looked[j - diag], 0))) break;
-#pragma unroll 1
-            for (int t = 0; t < 2; ++t) {
-              if (j >= (t ? n1 : n0)) continue;
-              if (!wait(&sh.p_full[t][MODE == kSplit ? j & 1 : 0], (MODE == kSplit ? j >> 1 : j) & 1)) break;
+            for (int j = 0; j < w.nt && ok; ++j) {
+              const bool first = j < w.n0, second = j < w.n1;
+              // The place for the scores is free: a tile is the c-th (16-bit) or c / 2-th one there.
+              const int b0 = MODE == kSplit ? c0 & 1 : 0, b1 = MODE == kSplit ? c1 & 1 : 0;
+              const int p0 = (MODE == kSplit ? c0 >> 1 : c0) & 1, p1 = (MODE == kSplit ? c1 >> 1 : c1) & 1;
+              if (!full(k_slot(j)) || (first && !wait(&sh.s_free[0][b0], p0 ^ 1)) ||
+                  (second && !wait(&sh.s_free[1][b1], p1 ^ 1)))
+                break;
+              if (j == 0 && !(wait(&sh.q_full[buf][0], it / C::QBufs & 1) &&
+                              (!second || wait(&sh.q_full[buf][1], it / C::QBufs & 1))))
+                break;
               ptx::tc_fence_after();
-              values(t, j, t == 1 || j >= n1);
+              scores(j, buf, c0, c1, first, second);
+              c0 += first;
+              c1 += second;
+            }
+          } else {
+#pragma unroll 1
+            for (int j = 0; j < w.nt && ok; ++j) {
+              const int look = looks + j - w.diag, slot = v_slot(j, w.nt);
+              if (!full(slot) || (j >= w.diag && !wait(&sh.looked[look % kLooks], look / kLooks & 1))) break;
+#pragma unroll 1
+              for (int t = 0; t < 2; ++t) {
+                if (j >= (t ? w.n1 : w.n0)) continue;
+                const int c = t ? c1 : c0;
+                if (!wait(&sh.p_full[t][MODE == kSplit ? c & 1 : 0], (MODE == kSplit ? c >> 1 : c) & 1)) break;
+                ptx::tc_fence_after();
+                values(t, j, c, slot % ST, t == 1 || j >= w.n1);
+                if (t) ++c1;
+                else ++c0;
+              }
             }
           }
+          if (!ok) break;
+          advance(w);
         }
         if (ptx::elect_one()) ptx::tc_commit(&sh.drain);
       }
@@ -455,57 +556,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t kExp = MODE == kBf16 ? 0x7f807f80u : 0x7c007c00u;
       constexpr uint32_t kOne = MODE == kBf16 ? 0x00800080u : 0x04000400u;
       bool ok = true;
-      for (int j = diag; j < nt && ok; ++j) {
-        const int i = v_slot(j);
-        // The slot's phase is this tile's from the copy's start until the tile has been looked at: only
-        // then does its parity mean this tile.
-        ok = warp_wait(&sh.look[j - diag], 0, a.wait_limit, abort) &&
-             warp_wait(&sh.kv_full[i % ST], (i / ST) & 1, a.wait_limit, abort);
+#pragma unroll 1
+      for (int it = 0; ok; ++it) {
+        ok = warp_wait(&sh.item_full[it & 1], it >> 1 & 1, a.wait_limit, abort);
         if (!ok) {
           record_timeout(abort);
           break;
         }
-        // The high plane; the other is finite in the sequence's rows, and unknown behind them.
-        uint4 *tile = reinterpret_cast<uint4 *>(smem_kv + (i % ST) * C::KvBytes);
-        const int planes = (j + 1) * BK > len ? C::Parts : 1;
-        // Exponents of ones only, in two halves of a word at once: adding one to such an exponent sets the sign.
-        auto check = [](const uint4 &x) {
-          return (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) &
-                 0x80008000u;
-        };
-        const int pieces = planes * BK * D / 8;
-        uint32_t bad = 0;
-#pragma unroll 8
-        for (int c = lane; c < pieces; c += 32) bad |= check(tile[c]);
-        if (__any_sync(0xffffffffu, bad != 0)) {
-          bool mine = false;
-          for (int c = lane; c < pieces; c += 32) {
-            uint4 x = tile[c];
-            if (!check(x)) continue;
-            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t b = ((w[k] & kExp) + kOne) & 0x80008000u;
-              if (b & 0x8000u) w[k] &= 0xffff0000u;
-              if (b & 0x80000000u) w[k] &= 0xffffu;
-            }
-            tile[c] = x;
-            mine |= j * BK + c / 8 % BK < len;  // not of the rows behind the sequence
-          }
-          if (mine) sh.nonfinite = 1;
-          ptx::fence_proxy_async_smem();
-        }
+        const Work w = read_item(it);
+        if (w.len == 0) break;
+        const int len = w.len;
+        if (lane == 0) sh.nonfinite[it & 1] = 0;
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.looked[j - diag]);
+        for (int j = w.diag; j < w.nt && ok; ++j) {
+          const int i = v_slot(j, w.nt), look = looks + j - w.diag;
+          // The slot's phase is this tile's from the copy's start until the tile has been looked at: only
+          // then does its parity mean this tile.
+          ok = warp_wait(&sh.look[look % kLooks], look / kLooks & 1, a.wait_limit, abort) &&
+               warp_wait(&sh.kv_full[i % ST], (i / ST) & 1, a.wait_limit, abort);
+          if (!ok) {
+            record_timeout(abort);
+            break;
+          }
+          // The high plane; the other is finite in the sequence's rows, and unknown behind them.
+          uint4 *tile = reinterpret_cast<uint4 *>(smem_kv + (i % ST) * C::KvBytes);
+          const int planes = (j + 1) * BK > w.len ? C::Parts : 1;
+          // Exponents of ones only, in two halves of a word at once: adding one to such an exponent sets the sign.
+          auto check = [](const uint4 &x) {
+            return (((x.x & kExp) + kOne) | ((x.y & kExp) + kOne) | ((x.z & kExp) + kOne) | ((x.w & kExp) + kOne)) &
+                   0x80008000u;
+          };
+          const int pieces = planes * BK * D / 8;
+          uint32_t bad = 0;
+#pragma unroll 8
+          for (int c = lane; c < pieces; c += 32) bad |= check(tile[c]);
+          if (__any_sync(0xffffffffu, bad != 0)) {
+            bool mine = false;
+            for (int c = lane; c < pieces; c += 32) {
+              uint4 x = tile[c];
+              if (!check(x)) continue;
+              uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t b = ((w[k] & kExp) + kOne) & 0x80008000u;
+                if (b & 0x8000u) w[k] &= 0xffff0000u;
+                if (b & 0x80000000u) w[k] &= 0xffffu;
+              }
+              tile[c] = x;
+              mine |= j * BK + c / 8 % BK < len;  // not of the rows behind the sequence
+            }
+            if (mine) sh.nonfinite[it & 1] = 1;
+            ptx::fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.looked[look % kLooks]);
+        }
+        if (!ok) break;
+        // One phase an item: the query warps have to be behind the last one.
+        ok = it == 0 || warp_wait(&sh.done[(it - 1) & 1], (it - 1) >> 1 & 1, a.wait_limit, abort);
+        if (!ok) {
+          record_timeout(abort);
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive(&sh.looked_all);
+        advance(w);
       }
-      if (lane == 0) ptx::mbar_arrive(&sh.looked_all);
     }
   } else {
     // ---- a query tile: one row a thread ----
     ptx::regs_inc<C::QueryRegs>();
     const int t = warp >> 2;
-    const int row = r0 + t * kRows + (threadIdx.x & 127);
-    const int n = t ? n1 : n0;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * kScores, t_addr = tmem + lanes + kTile + t * D;
     bool ok = true;
@@ -516,272 +636,281 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return ok;
     };
-    // The output goes by way of the query tile's place in shared memory, idle after its last scores, so that a
-    // warp's stores are whole rows: written a row a lane, they took as long as three tiles.
-    constexpr int kChunks = D * (MODE == kSplit ? 4 : 2) / 16;  // 16-byte pieces of a row
-    auto stage = [&](int r, int chunk) {
-      return reinterpret_cast<uint4 *>(smem + t * C::QBytes) + r * kChunks + (chunk ^ (r & 7));
-    };
-    auto write_rows = [&] {
-      __syncwarp();
-      uint8_t *out = static_cast<uint8_t *>(a.o.data);
-      constexpr int kSize = MODE == kSplit ? 4 : 2;
-#pragma unroll 4
-      for (int i = lane; i < 32 * kChunks; i += 32) {
-        const int r = (warp & 3) * 32 + i / kChunks, chunk = i % kChunks, to = r0 + t * kRows + r;
-        if (to < len)
-          *reinterpret_cast<uint4 *>(out + ((start + to) * a.o.row_stride + head * a.o.head_stride) * kSize +
-                                     16 * chunk) = *stage(r, chunk);
-      }
-      __syncwarp();
-      if (sh.nonfinite && row < len)
-        add_nonfinite<D>(out + ((start + row) * a.o.row_stride + head * a.o.head_stride) * kSize,
-                         static_cast<const uint8_t *>(a.v.data) +
-                             ((start + diag * BK) * a.v.row_stride + kv_head * a.v.head_stride) * kSize,
-                         a.v.row_stride, row - diag * BK + 1, a.v.dtype);
-    };
-    if constexpr (MODE != kSplit) {
-      // 16-bit rows: a tile's scores in registers, the output summed in tensor memory. The weights
-      // are taken against `ref`, a maximum that may lag behind: only when a row's maximum has grown by more
-      // than 2^8 is the row's output scaled down (by its own thread), which a few tiles at a row's
-      // start need. The largest weight is then 2^8, which both types hold.
-      float ref = 0, l = 0;
-      const float c = a.scale;
+    int count = 0;  // tiles before this item's
 #pragma unroll 1
-      for (int j = 0; j < n; ++j) {
-        if (!wait(&sh.s_full[t][0], j & 1)) break;
-        ptx::tc_fence_after();
-        uint32_t x[BK / 16][16];
-#pragma unroll
-        for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_32x32b_x16(s_addr + 16 * ch, x[ch]);
-#pragma unroll
-        for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_wait(x[ch]);
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.s_free[t][0]);
-        const int lim = row - j * BK;  // the last column that this row sees
-        const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < BK; ++i)
-            if (i > lim) x[i >> 4][i & 15] = 0xff800000u;
-        }
-        float mx[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(x[0][i]);
-#pragma unroll
-        for (int i = 4; i < BK; i += 8)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {  // pairs i + 2 k, i + 2 k + 1 (the last group has one pair for two maxima)
-            const int e = i + 2 * k;
-            if (e + 1 < BK) mx[k] = max3(mx[k], __uint_as_float(x[e >> 4][e & 15]), __uint_as_float(x[(e + 1) >> 4][(e + 1) & 15]));
-          }
-        // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
-        const float m = fmaxf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c, -3.402823466e38f);
-        // The last product is complete, its weights and its sum are free to be written.
-        if (j > 0) {
-          if (!wait(&sh.t_full[t], (j - 1) & 1)) break;
-          ptx::tc_fence_after();
-        }
-        if (j == 0) {
-          ref = m;
-        } else if (__any_sync(0xffffffffu, m > ref + 8.0f)) {
-          const float next = fmaxf(ref, m), alpha = ex2(ref - next);
-          const float2 al = make_float2(alpha, alpha);
-          ref = next;
-          l *= alpha;
-#pragma unroll
-          for (int ch = 0; ch < D / 16; ++ch) {
-            uint32_t y[16];
-            ptx::tmem_ld_32x32b_x16(t_addr + 16 * ch, y);
-            ptx::tmem_ld_wait(y);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float2 z = __fmul2_rn(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), al);
-              y[i] = __float_as_uint(z.x);
-              y[i + 1] = __float_as_uint(z.y);
-            }
-            ptx::tmem_st_32x32b_x16(t_addr + 16 * ch, y);
-          }
-        }
-        const float2 cc = make_float2(c, c), rr = make_float2(-ref, -ref);
-        float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
-#pragma unroll
-        for (int ch = 0; ch < BK / 16; ++ch) {
-          uint32_t w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            float2 y =
-                __ffma2_rn(make_float2(__uint_as_float(x[ch][2 * i]), __uint_as_float(x[ch][2 * i + 1])), cc, rr);
-            y = make_float2(ex2(y.x), ex2(y.y));
-            sum[i & 1] = __fadd2_rn(sum[i & 1], y);
-            w[i] = pack<MODE>(y.x, y.y);
-          }
-          ptx::tmem_st_32x32b_x8(s_addr + BK + 8 * ch, w);
-        }
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);
-      }
-      if (ok && n > 0) wait(&sh.t_full[t], (n - 1) & 1);
-      if (ok && n > 0) wait(&sh.looked_all, 0);
-      if (ok && n > 0) {
-        ptx::tc_fence_after();
-        const float inv = 1.0f / l;
-#pragma unroll 1
-        for (int ch = 0; ch < D / 32; ++ch) {
-          uint32_t y[32];
-          __syncwarp();
-          ptx::tmem_ld_32x32b_x32(t_addr + 32 * ch, y);
-          ptx::tmem_ld_wait(y);
-          float o[32];
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(y[i]) * inv;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *stage(threadIdx.x & 127, 4 * ch + i) =
-                make_uint4(pack<MODE>(o[8 * i], o[8 * i + 1]), pack<MODE>(o[8 * i + 2], o[8 * i + 3]),
-                           pack<MODE>(o[8 * i + 4], o[8 * i + 5]), pack<MODE>(o[8 * i + 6], o[8 * i + 7]));
-        }
-        write_rows();
-      }
-    } else {
-      float2 o[D / 2];
-#pragma unroll
-      for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0, 0);
-      float m = -INFINITY, l = 0, alpha = 0, v_pow = 1;
-      float scale = a.scale;
-      const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
-      if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
-      // o = o alpha + a tile's product
-      auto accumulate = [&](int j, float alpha, float v_pow) {
-        if (!wait(&sh.t_full[t], j & 1)) return;
-        ptx::tc_fence_after();
-        const float2 al = make_float2(alpha, alpha), vp = make_float2(v_pow, v_pow);
-        uint32_t x[2][32];
-        ptx::tmem_ld_32x32b_x32(t_addr, x[0]);
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          ptx::tmem_ld_wait(x[c & 1]);
-          if (c + 1 < D / 32) ptx::tmem_ld_32x32b_x32(t_addr + 32 * (c + 1), x[(c + 1) & 1]);
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 y = make_float2(__uint_as_float(x[c & 1][2 * i]), __uint_as_float(x[c & 1][2 * i + 1]));
-            float2 &z = o[16 * c + i];
-            z = __ffma2_rn(z, al, __fmul2_rn(y, vp));
-          }
-        }
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(j + 1) & 1]);
+    for (int it = 0; wait(&sh.item_full[it & 1], it >> 1 & 1); ++it) {
+      const Work w = read_item(it);
+      if (w.len == 0) break;
+      const int head = w.head, start = w.start, len = w.len, r0 = w.r0, diag = w.diag, kv_head = w.head / a.group;
+      const int row = r0 + t * kRows + (threadIdx.x & 127);
+      const int n = t ? w.n1 : w.n0;
+      // The output goes by way of the query tile's place in shared memory, idle after its last scores, so that a
+      // warp's stores are whole rows: written a row a lane, they took as long as three tiles.
+      constexpr int kChunks = D * (MODE == kSplit ? 4 : 2) / 16;  // 16-byte pieces of a row
+      auto stage = [&](int r, int chunk) {
+        return reinterpret_cast<uint4 *>(smem + (it % C::QBufs * 2 + t) * C::QBytes) + r * kChunks + (chunk ^ (r & 7));
       };
-      // A tile's weights come before the tile before it is added, whose factors are kept until then.
+      auto write_rows = [&] {
+        __syncwarp();
+        uint8_t *out = static_cast<uint8_t *>(a.o.data);
+        constexpr int kSize = MODE == kSplit ? 4 : 2;
+#pragma unroll 4
+        for (int i = lane; i < 32 * kChunks; i += 32) {
+          const int r = (warp & 3) * 32 + i / kChunks, chunk = i % kChunks, to = r0 + t * kRows + r;
+          if (to < len)
+            *reinterpret_cast<uint4 *>(out + ((start + to) * a.o.row_stride + head * a.o.head_stride) * kSize +
+                                       16 * chunk) = *stage(r, chunk);
+        }
+        __syncwarp();
+        if (sh.nonfinite[it & 1] && row < len)
+          add_nonfinite<D>(out + ((start + row) * a.o.row_stride + head * a.o.head_stride) * kSize,
+                           static_cast<const uint8_t *>(a.v.data) +
+                               ((start + diag * BK) * a.v.row_stride + kv_head * a.v.head_stride) * kSize,
+                           a.v.row_stride, row - diag * BK + 1, a.v.dtype);
+      };
+      if constexpr (MODE != kSplit) {
+        // 16-bit rows: a tile's scores in registers, the output summed in tensor memory. The weights
+        // are taken against `ref`, a maximum that may lag behind: only when a row's maximum has grown by more
+        // than 2^8 is the row's output scaled down (by its own thread), which a few tiles at a row's
+        // start need. The largest weight is then 2^8, which both types hold.
+        float ref = 0, l = 0;
+        const float c = a.scale;
 #pragma unroll 1
-      for (int j = 0; j < n && ok; ++j) {
-        const int64_t at = pow0 + min(static_cast<int64_t>(sh.tile0) + j, a.tiles - 1);
-        const float k_pow = __ldg(a.k_pow + at), v_next = __ldg(a.v_pow + at);
-        if (!wait(&sh.s_full[t][j & 1], (j >> 1) & 1)) break;
-        ptx::tc_fence_after();
-        const uint32_t s_addr = tmem + lanes + t * kScores + (j & 1) * BK;
-        const float alpha_last = alpha;
-        const float c = scale * k_pow;
-        const int lim = row - j * BK;  // the last column that this row sees
-        const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
-        // Four maxima and four pairs of sums, so that no addition waits for the one before.
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        float2 sum[4];
-        float2 ref;
-        const float2 cc = make_float2(c, c);
-        auto start_load = [&](int ch, uint32_t (&x)[32]) { ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x); };
-        auto mask = [&](int ch, uint32_t (&x)[32]) {
+        for (int j = 0; j < n; ++j) {
+          if (!wait(&sh.s_full[t][0], (count + j) & 1)) break;
+          ptx::tc_fence_after();
+          uint32_t x[BK / 16][16];
+#pragma unroll
+          for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_32x32b_x16(s_addr + 16 * ch, x[ch]);
+#pragma unroll
+          for (int ch = 0; ch < BK / 16; ++ch) ptx::tmem_ld_wait(x[ch]);
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.s_free[t][0]);
+          const int lim = row - j * BK;  // the last column that this row sees
+          const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
           if (masked) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * ch + i > lim) x[i] = 0xff800000u;
+            for (int i = 0; i < BK; ++i)
+              if (i > lim) x[i >> 4][i & 15] = 0xff800000u;
           }
-        };
-        auto top = [&](const uint32_t (&x)[32]) {
+          float mx[4];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-        };
-        auto settle = [&] {
-          const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(x[0][i]);
+#pragma unroll
+          for (int i = 4; i < BK; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {  // pairs i + 2 k, i + 2 k + 1 (the last group has one pair for two maxima)
+              const int e = i + 2 * k;
+              if (e + 1 < BK)
+                mx[k] = max3(mx[k], __uint_as_float(x[e >> 4][e & 15]), __uint_as_float(x[(e + 1) >> 4][(e + 1) & 15]));
+            }
           // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
-          const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
-          const float r = 13.0f - m2;
-          ref = make_float2(r, r);
-          alpha = ex2(m - m2);
-          l *= alpha;
-          m = m2;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[i] = make_float2(0, 0);
-        };
-        // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
-        auto weights = [&](int ch, const uint32_t (&x)[32]) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
-            y = make_float2(ex2(y.x), ex2(y.y));
-            sum[i & 3] = __fadd2_rn(sum[i & 3], y);
-            hi[i] = pack<MODE>(y.x, y.y);
-            const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
-            const float2 rest = __fadd2_rn(y, make_float2(-h.x, -h.y));
-            lo[i] = pack<MODE>(rest.x, rest.y);
+          const float m = fmaxf(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * c, -3.402823466e38f);
+          // The last product is complete, its weights and its sum are free to be written.
+          if (j > 0) {
+            if (!wait(&sh.t_full[t], (count + j - 1) & 1)) break;
+            ptx::tc_fence_after();
           }
-          ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
-          ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+          if (j == 0) {
+            ref = m;
+          } else if (__any_sync(0xffffffffu, m > ref + 8.0f)) {
+            const float next = fmaxf(ref, m), alpha = ex2(ref - next);
+            const float2 al = make_float2(alpha, alpha);
+            ref = next;
+            l *= alpha;
+#pragma unroll
+            for (int ch = 0; ch < D / 16; ++ch) {
+              uint32_t y[16];
+              ptx::tmem_ld_32x32b_x16(t_addr + 16 * ch, y);
+              ptx::tmem_ld_wait(y);
+#pragma unroll
+              for (int i = 0; i < 16; i += 2) {
+                const float2 z = __fmul2_rn(make_float2(__uint_as_float(y[i]), __uint_as_float(y[i + 1])), al);
+                y[i] = __float_as_uint(z.x);
+                y[i + 1] = __float_as_uint(z.y);
+              }
+              ptx::tmem_st_32x32b_x16(t_addr + 16 * ch, y);
+            }
+          }
+          const float2 cc = make_float2(c, c), rr = make_float2(-ref, -ref);
+          float2 sum[2] = {make_float2(0, 0), make_float2(0, 0)};
+#pragma unroll
+          for (int ch = 0; ch < BK / 16; ++ch) {
+            uint32_t w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              float2 y =
+                  __ffma2_rn(make_float2(__uint_as_float(x[ch][2 * i]), __uint_as_float(x[ch][2 * i + 1])), cc, rr);
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sum[i & 1] = __fadd2_rn(sum[i & 1], y);
+              w[i] = pack<MODE>(y.x, y.y);
+            }
+            ptx::tmem_st_32x32b_x8(s_addr + BK + 8 * ch, w);
+          }
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);
+        }
+        if (ok && n > 0) wait(&sh.t_full[t], (count + n - 1) & 1);
+        if (ok && n > 0) wait(&sh.looked_all, it & 1);
+        if (ok && n > 0) {
+          ptx::tc_fence_after();
+          const float inv = 1.0f / l;
+#pragma unroll 1
+          for (int ch = 0; ch < D / 32; ++ch) {
+            uint32_t y[32];
+            __syncwarp();
+            ptx::tmem_ld_32x32b_x32(t_addr + 32 * ch, y);
+            ptx::tmem_ld_wait(y);
+            float o[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __uint_as_float(y[i]) * inv;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *stage(threadIdx.x & 127, 4 * ch + i) =
+                  make_uint4(pack<MODE>(o[8 * i], o[8 * i + 1]), pack<MODE>(o[8 * i + 2], o[8 * i + 3]),
+                             pack<MODE>(o[8 * i + 4], o[8 * i + 5]), pack<MODE>(o[8 * i + 6], o[8 * i + 7]));
+          }
+          write_rows();
+        }
+      } else {
+        float2 o[D / 2];
+#pragma unroll
+        for (int i = 0; i < D / 2; ++i) o[i] = make_float2(0, 0);
+        float m = -INFINITY, l = 0, alpha = 0, v_pow = 1;
+        float scale = a.scale;
+        const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
+        const int tile0 = sh.item[it & 1].tile0;
+        if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
+        // o = o alpha + a tile's product
+        auto accumulate = [&](int j, float alpha, float v_pow) {
+          if (!wait(&sh.t_full[t], (count + j) & 1)) return;
+          ptx::tc_fence_after();
+          const float2 al = make_float2(alpha, alpha), vp = make_float2(v_pow, v_pow);
+          uint32_t x[2][32];
+          ptx::tmem_ld_32x32b_x32(t_addr, x[0]);
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            ptx::tmem_ld_wait(x[c & 1]);
+            if (c + 1 < D / 32) ptx::tmem_ld_32x32b_x32(t_addr + 32 * (c + 1), x[(c + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float2 y = make_float2(__uint_as_float(x[c & 1][2 * i]), __uint_as_float(x[c & 1][2 * i + 1]));
+              float2 &z = o[16 * c + i];
+              z = __ffma2_rn(z, al, __fmul2_rn(y, vp));
+            }
+          }
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(count + j + 1) & 1]);
         };
-        uint32_t x0[32], x1[32];
-        start_load(0, x0);
-        ptx::tmem_ld_wait(x0);
-        start_load(1, x1);
-        mask(0, x0);
-        top(x0);
-        ptx::tmem_ld_wait(x1);
-        mask(1, x1);  // both are read before the weights overwrite them
-        top(x1);
-        settle();
-        weights(0, x0);
-        weights(1, x1);
+        // A tile's weights come before the tile before it is added, whose factors are kept until then.
+#pragma unroll 1
+        for (int j = 0; j < n && ok; ++j) {
+          const int64_t at = pow0 + min(static_cast<int64_t>(tile0) + j, a.tiles - 1);
+          const float k_pow = __ldg(a.k_pow + at), v_next = __ldg(a.v_pow + at);
+          const int b = (count + j) & 1;
+          if (!wait(&sh.s_full[t][b], (count + j) >> 1 & 1)) break;
+          ptx::tc_fence_after();
+          const uint32_t s_addr = tmem + lanes + t * kScores + b * BK;
+          const float alpha_last = alpha;
+          const float c = scale * k_pow;
+          const int lim = row - j * BK;  // the last column that this row sees
+          const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
+          // Four maxima and four pairs of sums, so that no addition waits for the one before.
+          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float2 sum[4];
+          float2 ref;
+          const float2 cc = make_float2(c, c);
+          auto start_load = [&](int ch, uint32_t (&x)[32]) { ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x); };
+          auto mask = [&](int ch, uint32_t (&x)[32]) {
+            if (masked) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) l += sum[i].x + sum[i].y;
-        ptx::tmem_st_wait();
-        ptx::tc_fence_before();
+              for (int i = 0; i < 32; ++i)
+                if (32 * ch + i > lim) x[i] = 0xff800000u;
+            }
+          };
+          auto top = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+          };
+          auto settle = [&] {
+            const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
+            const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
+            const float r = 13.0f - m2;
+            ref = make_float2(r, r);
+            alpha = ex2(m - m2);
+            l *= alpha;
+            m = m2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0, 0);
+          };
+          // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
+          auto weights = [&](int ch, const uint32_t (&x)[32]) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
+              y = make_float2(ex2(y.x), ex2(y.y));
+              sum[i & 3] = __fadd2_rn(sum[i & 3], y);
+              hi[i] = pack<MODE>(y.x, y.y);
+              const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+              const float2 rest = __fadd2_rn(y, make_float2(-h.x, -h.y));
+              lo[i] = pack<MODE>(rest.x, rest.y);
+            }
+            ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
+            ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+          };
+          uint32_t x0[32], x1[32];
+          start_load(0, x0);
+          ptx::tmem_ld_wait(x0);
+          start_load(1, x1);
+          mask(0, x0);
+          top(x0);
+          ptx::tmem_ld_wait(x1);
+          mask(1, x1);  // both are read before the weights overwrite them
+          top(x1);
+          settle();
+          weights(0, x0);
+          weights(1, x1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) l += sum[i].x + sum[i].y;
+          ptx::tmem_st_wait();
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][b]);
+          if (j > 0) accumulate(j - 1, alpha_last, v_pow);
+          else if (count == 0 && lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);  // nothing to read out yet
+          v_pow = v_next;
+        }
+        if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
+        if (ok && n > 0) wait(&sh.looked_all, it & 1);
+        if (ok && row < len) {
+          const float inv = 1.0f / l;
+#pragma unroll
+          for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
+#pragma unroll
+          for (int i = 0; i < D / 4; ++i)
+            *stage(threadIdx.x & 127, i) = make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
+                                                      __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y));
+        }
         __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][j & 1]);
-        if (j > 0) accumulate(j - 1, alpha_last, v_pow);
-        else if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);  // nothing to read out yet
-        v_pow = v_next;
+        if (ok && n > 0) write_rows();
       }
-      if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
-      if (ok && n > 0) wait(&sh.looked_all, 0);
-      if (ok && row < len) {
-        const float inv = 1.0f / l;
-#pragma unroll
-        for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
-#pragma unroll
-        for (int i = 0; i < D / 4; ++i)
-          *stage(threadIdx.x & 127, i) = make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y),
-                                                    __float_as_uint(o[2 * i + 1].x), __float_as_uint(o[2 * i + 1].y));
-      }
+      if (!ok) break;
+      count += n;
+      // the copies of other queries into these rows' place come after what is read from it here
+      ptx::fence_proxy_async_smem();
       __syncwarp();
-      if (ok && n > 0) write_rows();
+      if (lane == 0) ptx::mbar_arrive(&sh.done[it & 1]);
     }
   }
 
   // ---- teardown: what this block has in flight ends, then its tensor memory is freed ----
-  if (*abort) {
-    int no_abort = 0;
-    if (warp == 8 && lane == 0) {
-      ptx::mbar_wait_bounded(&sh.q_full[0], 0, kDrainLimit, &no_abort);
-      if (n1 > 0) ptx::mbar_wait_bounded(&sh.q_full[1], 0, kDrainLimit, &no_abort);
-      for (int i = max(0, issued - ST); i < issued; ++i)
-        ptx::mbar_wait_bounded(&sh.kv_full[i % ST], (i / ST) & 1, kDrainLimit, &no_abort);
-    }
-  }
   if (warp == 9 && lane == 0) {
     int no_abort = 0;
     ptx::mbar_wait_bounded(&sh.drain, 0, kDrainLimit, &no_abort);

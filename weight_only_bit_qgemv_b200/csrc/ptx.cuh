@@ -146,6 +146,31 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
       : "memory");
 }
 
+// Cluster launch control: asks for a block of this grid that has not started, which then never does; the answer
+// arrives at dst (16 bytes) and on bar.
+__device__ __forceinline__ void claim_block(uint4 *dst, uint64_t *bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(dst)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// Whether the claim got one, and its blockIdx.x.
+__device__ __forceinline__ bool claimed_block(const uint4 *answer, uint32_t *x) {
+  uint32_t ok, id;
+  asm volatile(
+      "{.reg .b128 r; .reg .pred p;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t"
+      "mov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;}"
+      : "=r"(ok), "=r"(id)
+      : "r"(smem_u32(answer))
+      : "memory");
+  *x = id;
+  return ok != 0;
+}
+
 // ---- tcgen05 -----------------------------------------------------------------------------
 __device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
