@@ -39,39 +39,41 @@ __device__ __forceinline__ int value_halfword(int h) {
 // quotients are approximated, and computed as written only where the approximation could round otherwise:
 //   - a * (1 / 7) is off by less than 2 ulp: written out where its 13 bits below binary16's are within 4 of a half,
 //     or where binary16 is subnormal (then the code may need the clamp, too);
-//   - x * (1 / s) + 768.5, whose last bit is 2^-14, is off by less than 2^-14: written out where its 14 fraction bits
-//     are within 1 of a whole number. Above them is round(x / s) in two's complement.
+//   - x * (1 / s) + 192.5, whose last bit is 2^-16, is off by less than 2^-16: written out where its 16 fraction bits
+//     are within 1 of a whole number, which is 0 to 2 after adding that 1. Above them, from the third byte on, is
+//     round(x / s) in two's complement.
 // Written out, x / s is a correctly rounded 32-bit quotient. That is enough: s has 11 significant bits, so
 // (k + 1/2) s is exact in 24, and an x next to it differs from it by at least an ulp of x, more than 2^-24 of it,
 // while half an ulp of the quotient is at most 2^-24 of it: a quotient that is not a tie cannot become one.
 // A block with a NaN or with a scale beyond binary16 becomes NaN as a whole: scale NaN, codes 0.
 __device__ __forceinline__ uint32_t quantise(float4 x, uint16_t *scale) {
-  auto abs_bits = [](float f) { return __float_as_uint(f) & 0x7fffffffu; };
-  // as whole numbers, where infinity and NaN are above all others
-  uint32_t big = max(max(abs_bits(x.x), abs_bits(x.y)), max(abs_bits(x.z), abs_bits(x.w)));
+  float a;  // NaN if one of them is
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x.x), "f"(x.y), "f"(x.z));
+  asm("max.NaN.abs.f32 %0, %0, %1, %1;" : "+f"(a) : "f"(x.w));
 #pragma unroll
-  for (int i = 1; i < 8; i <<= 1) big = max(big, __shfl_xor_sync(0xffffffffu, big, i));
-  const float a = __uint_as_float(big), q = a * 0.142857142857f;
+  for (int i = 1; i < 8; i <<= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, a, i);
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(other));
+  }
+  const float q = a * 0.142857142857f;
   __half h = __float2half_rn(q);
   bool exactly = q < 6.2e-5f;
   if (exactly || ((__float_as_uint(q) + 4u - 0x1000u) & 0x1fffu) <= 8u)
     h = __double2half(__ddiv_rn(static_cast<double>(a), 7.0));
-  if (big >= 0x7f800000u || __hisinf(h)) {
+  const float s = __half2float(h);
+  if (!(s < INFINITY)) {
     *scale = 0x7fffu;
     return 0;
   }
   *scale = __half_as_ushort(h);
-  const float s = __half2float(h);
   float inv;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
   const float v[4] = {x.x, x.y, x.z, x.w};
-  uint32_t code = 0, least = 0x3fffu;
+  uint32_t t[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t t = __float_as_uint(fmaf(v[i], inv, 768.5f));
-    least = min(least, (t + 1u) & 0x3fffu);
-    code |= (t >> 14 & 15u) << 4 * i;
-  }
+  for (int i = 0; i < 4; ++i) t[i] = __float_as_uint(fmaf(v[i], inv, 192.5f + 0x1p-16f));
+  const uint32_t least = min(__vimin3_u32(t[0] << 16, t[1] << 16, t[2] << 16), t[3] << 16) >> 16;
+  uint32_t code = (__byte_perm(t[0], t[2], 0x0062) & 0x0f0fu) | (__byte_perm(t[1], t[3], 0x0062) << 4 & 0xf0f0u);
   if (exactly || least <= 2u) {
     code = 0;
     if (s != 0.0f) {
@@ -122,7 +124,7 @@ struct Args {
 //
 // A warp takes `per` consecutive pieces (a token's pair of heads), so that it looks a token's page up once, and
 // appending, it has the next piece's rows under way while it quantises this one's.
-template <int D, bool APPEND>
+template <int D, bool APPEND, bool F32>
 __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
   constexpr int NB = D / 32, LANES = D / 4, ROWS = 2 * D / 128;  // ROWS: rows a lane has of each head
   ptx::pdl_wait();
@@ -143,7 +145,7 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
         const woq_rows &src = (ROWS == 2 ? r : part) ? a.v : a.k;
         x[i][r] = make_float4(0, 0, 0, 0);
         if (h0 + i < a.heads)
-          x[i][r] = load4(src.data, t * src.row_stride + (h0 + i) * src.head_stride + 4 * h, src.dtype);
+          x[i][r] = load4(src.data, t * src.row_stride + (h0 + i) * src.head_stride + 4 * h, F32 ? WOQ_F32 : src.dtype);
       }
   };
   int64_t t = first / a.chunks;
@@ -203,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
           const woq_rows &dst = kv ? a.v : a.k;
           const float s = __half2float(__ushort_as_half(sc[i][r]));
           const int c = static_cast<int>(w[i][r]) << 16;  // sign-extend each nibble from the top
-          store4(dst.data, token * dst.row_stride + hd * dst.head_stride + 4 * h, dst.dtype,
+          store4(dst.data, token * dst.row_stride + hd * dst.head_stride + 4 * h, F32 ? WOQ_F32 : dst.dtype,
                  make_float4(s * static_cast<float>(c << 12 >> 28), s * static_cast<float>(c << 8 >> 28),
                              s * static_cast<float>(c << 4 >> 28), s * static_cast<float>(c >> 28)));
         }
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
   }
 }
 
-template <int D, bool APPEND>
+template <int D, bool APPEND, bool F32>
 int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
   // One piece a warp while they fit the device at once, then as many waves as keep a warp at 8 at most.
   const int64_t items = a.tokens * a.chunks, in_block = kThreads / 32;
@@ -228,7 +230,7 @@ int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, APPEND>, b) != cudaSuccess) return WOQ_ECUDA;
+  if (cudaLaunchKernelEx(&cfg, kv4_rows_kernel<D, APPEND, F32>, b) != cudaSuccess) return WOQ_ECUDA;
   count_launches(1);
   return WOQ_OK;
 }
@@ -253,8 +255,15 @@ int launch_kv4_rows(const woq_kv4 &c, const woq_rows &k, const woq_rows &v, int6
   a.shift = __builtin_ctz(static_cast<unsigned>(c.page));
   a.heads = c.kv_heads;
   a.chunks = (c.kv_heads + kHeadsPerWarp - 1) / kHeadsPerWarp;
-  if (c.dim == 128) return append ? launch<128, true>(a, s, dev) : launch<128, false>(a, s, dev);
-  return append ? launch<64, true>(a, s, dev) : launch<64, false>(a, s, dev);
+  // float32 rows have kernels of their own: looking at the type takes as long as the address of a load.
+  const bool f32 = k.dtype == WOQ_F32 && v.dtype == WOQ_F32;
+  if (c.dim == 128)
+    return append ? f32 ? launch<128, true, true>(a, s, dev) : launch<128, true, false>(a, s, dev)
+           : f32  ? launch<128, false, true>(a, s, dev)
+                  : launch<128, false, false>(a, s, dev);
+  return append ? f32 ? launch<64, true, true>(a, s, dev) : launch<64, true, false>(a, s, dev)
+         : f32  ? launch<64, false, true>(a, s, dev)
+                : launch<64, false, false>(a, s, dev);
 }
 
 }  // namespace woq
