@@ -6,8 +6,10 @@
 // is three shuffles among eight lanes, and a lane's four codes are one 16-bit store into the row's
 // 64 bytes. The loads of both heads' keys and values are issued before any is used.
 //
-// Measured (8 key heads, dim 128, float32): 39,151 tokens are appended in 103 us
-// (3.6 TB/s: the quantiser's instructions) and gathered in 65 us (5.6 TB/s); 64 tokens in 3 us each.
+// Measured (8 key heads, dim 128, float32, a cold L2, a launch's time included): 39,151 tokens are appended in 98 us
+// (3.7 TB/s: the quantiser's instructions, two thirds of the cycles on the integer pipe) and gathered in 80 us
+// (4.6 TB/s); 64 tokens in 3 us each. Blocks of 256 threads 101 us; a fourth block of them an SM, 64 registers, 111;
+// 4 or 16 pieces a warp instead of 8, 104 and 110.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -17,7 +19,7 @@
 namespace woq {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kHeadsPerWarp = 2;
 
 // Where a lane's four values of a row are kept: the 16-bit halfword of the row.
@@ -219,7 +221,7 @@ int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
   // One piece a warp while they fit the device at once, then as many waves as keep a warp at 8 at most.
   const int64_t items = a.tokens * a.chunks, in_block = kThreads / 32;
   Args b = a;
-  b.per = std::min<int64_t>(8, std::max<int64_t>(1, items / (int64_t(dev.sm_count) * in_block * 4)));
+  b.per = std::min<int64_t>(8, std::max<int64_t>(1, items / (int64_t(dev.sm_count) * in_block * 8)));
   const int64_t warps = (items + b.per - 1) / b.per;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
