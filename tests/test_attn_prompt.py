@@ -263,3 +263,27 @@ def test_many_more_tiles_than_blocks_run_at_once(dtype, dim):
     if dtype != torch.float32:  # float32: such a value has no part in its tile's power of two
         assert torch.equal(got[~hit], out[~hit])
     assert woq.device_status() == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_thousands_of_sequences(dtype):
+    """Tiles are looked up among many sequences: 5000 of one to three rows and every other one empty."""
+    lens = [(i % 2) * (1 + i % 3) for i in range(10000)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).tolist()
+    q, k, v = fused(15, cu[-1], 3, 1, 64, dtype)
+    out = woq.attn_prompt(q, k, v, ints(cu))
+    seq = torch.repeat_interleave(torch.arange(len(lens), device="cuda"), torch.tensor(lens, device="cuda"))
+    x = torch.einsum("ihd,jd->hij", q.double(), k[:, 0].double()) / 8
+    row = torch.arange(cu[-1], device="cuda")
+    seen = (seq[:, None] == seq) & (row[:, None] >= row)
+    for i in range(0, cu[-1], 2000):
+        j = min(i + 2000, cu[-1])
+        p = torch.softmax(x[:, i:j].masked_fill(~seen[None, i:j], -torch.inf), -1)
+        want = torch.einsum("hij,jd->ihd", p, v[:, 0].double())
+        # exact()'s tolerance: three keys at most
+        size = torch.einsum("hij,jd->ihd", p, v[:, 0].double().abs())
+        e = (2.0**-20 if dtype == torch.float32 else 2.0**-58) + 2.0**-17
+        e = e * (q[i:j].double().abs().sum(-1) * k.double().abs().max() / 8)[..., None]  # above every sum |q k| scale
+        unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
+        assert ((out[i:j].double() - want).abs() <= (2 * e + 2.0**-18 + 2 * unit) * size + unit * want.abs()).all()
+    assert woq.device_status() == _lib.WOQ_OK

@@ -10,7 +10,7 @@
 namespace woq {
 namespace {
 
-constexpr int kMaxSequences = 1 << 20;
+constexpr int kMaxSequences = 1 << 16;  // a tile is looked up among them in a millisecond at most
 constexpr int kMaxGroup = 64;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }

@@ -33,9 +33,9 @@
 // every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory,
 // and added after the last tile to the rows that do see it.
 //
-// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20.5 us, 4096 238 us (28 of them the
-// planes; 0.98 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 718 us (146 the planes); 32,768 bfloat16
-// tokens 3.85 ms, 1.14 PFLOP/s, at the clock that the power cap leaves.
+// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20.5 us, 4096 235 us (28 of them the
+// planes; 1 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 711 us (146 the planes); 32,768 bfloat16
+// tokens 3.8 ms, 1.16 PFLOP/s, at the clock that the power cap leaves.
 #include <algorithm>
 #include <mutex>
 
@@ -147,15 +147,23 @@ __device__ __forceinline__ void record_timeout(volatile int *abort) {
 }
 
 // Tile `target` of all sequences' tiles of `rows` rows: its sequence's rows, its place there, and how
-// many tiles of kSplitRows the sequences before have. One warp. False if there are fewer tiles.
+// many tiles of kSplitRows the sequences before have. One warp. False if there are fewer tiles. The search goes on
+// where the warp's last one ended, if the target is not before that.
 struct Place {
   int start, len, tile, tiles, split0;
 };
-__device__ bool find_tile(const int32_t *cu, int batch, int64_t tokens, int64_t target, int rows, Place &p) {
+struct Cursor {
+  int b0;          // the first of 32 sequences
+  int64_t before;  // tiles of those before it
+  int split;       // and theirs of kSplitRows
+};
+__device__ bool find_tile(const int32_t *cu, int batch, int64_t tokens, int64_t target, int rows, Place &p,
+                          Cursor &at) {
   const int lane = threadIdx.x & 31;
-  int64_t before = 0;
-  int split = 0;
-  for (int b0 = 0; b0 < batch; b0 += 32) {
+  if (target < at.before) at = Cursor{};
+  int64_t before = at.before;
+  int split = at.split;
+  for (int b0 = at.b0; b0 < batch; b0 += 32) {
     const int b = b0 + lane;
     int64_t s = 0, e = 0;
     if (b < batch) {
@@ -177,6 +185,7 @@ __device__ bool find_tile(const int32_t *cu, int batch, int64_t tokens, int64_t 
     }
     const unsigned has = __ballot_sync(0xffffffffu, before + sum > target);
     if (has) {
+      at = Cursor{b0, before, split};
       const int l = __ffs(has) - 1;
       p.start = __shfl_sync(0xffffffffu, static_cast<int>(s), l);
       p.len = __shfl_sync(0xffffffffu, len, l);
@@ -300,8 +309,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   ptx::pdl_wait();
   Place place{};
+  Cursor cursor{};
   bool found = false;  // warp 8's: the item that it is about to hand out
-  if (warp == 8) found = find_tile(a.cu, a.batch, a.tokens, blockIdx.x / a.q_heads, kBlockRows, place);
+  if (warp == 8) found = find_tile(a.cu, a.batch, a.tokens, blockIdx.x / a.q_heads, kBlockRows, place, cursor);
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
@@ -422,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         uint32_t next;
         target = ptx::claimed_block(&sh.claim, &next) ? static_cast<int64_t>(next) : -1;
-        found = target >= 0 && find_tile(a.cu, a.batch, a.tokens, target / a.q_heads, kBlockRows, place);
+        found = target >= 0 && find_tile(a.cu, a.batch, a.tokens, target / a.q_heads, kBlockRows, place, cursor);
         __syncwarp();
       }
       if (*abort && lane == 0) {
@@ -961,8 +971,9 @@ __device__ __forceinline__ float largest(float4 x) {  // of what is finite
 // The power of two that a largest value in [2^13, 2^14) takes.
 __device__ __forceinline__ int exponent(float big) { return big > 0 ? max(min(ilogbf(big) - 13, 113), -113) : 0; }
 
-// Block (tile of 64 rows of a sequence, head of q, k or v): eight warps of eight rows, a lane four values of a row.
-template <int D>
+// Block (tile of 64 rows of a sequence, a head, or MANY of q, k and v): eight warps of eight rows, a lane four values of a
+// row.
+template <int D, bool MANY>
 __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const SplitArgs a) {
   constexpr int LANES = D / 4, ROWS = 8 * LANES / 32;  // rows that a lane has
   __shared__ Place place;
@@ -973,7 +984,8 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
     Place p{};
-    const bool f = find_tile(a.cu, a.batch, a.tokens, blockIdx.x, kSplitRows, p);
+    Cursor start{};
+    const bool f = find_tile(a.cu, a.batch, a.tokens, blockIdx.x, kSplitRows, p, start);
     if (lane == 0) {
       place = p;
       found = f;
@@ -981,50 +993,53 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
   }
   __syncthreads();
   if (!found) return;
-  const int hq = a.q.heads, hk = a.k.heads, y = blockIdx.y;
-  const int which = y < hq ? 0 : y < hq + hk ? 1 : 2;
-  const int head = which == 0 ? y : which == 1 ? y - hq : y - hq - hk;
-  const woq_rows &src = which == 0 ? a.q : which == 1 ? a.k : a.v;
-  const float *data = static_cast<const float *>(src.data);
-  const int col = 4 * (lane % LANES);
-  float4 x[ROWS];
-  int row[ROWS];
-  float big = 0;
+  const int hq = a.q.heads, hk = a.k.heads;
+  for (int y = blockIdx.y; MANY ? y < hq + 2 * hk : y == static_cast<int>(blockIdx.y); y += gridDim.y) {
+    const int which = y < hq ? 0 : y < hq + hk ? 1 : 2;
+    const int head = which == 0 ? y : which == 1 ? y - hq : y - hq - hk;
+    const woq_rows &src = which == 0 ? a.q : which == 1 ? a.k : a.v;
+    const float *data = static_cast<const float *>(src.data);
+    const int col = 4 * (lane % LANES);
+    float4 x[ROWS];
+    int row[ROWS];
+    float big = 0;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    row[i] = place.tile * kSplitRows + warp * 8 + i * (32 / LANES) + lane / LANES;
-    x[i] = make_float4(0, 0, 0, 0);
-    if (row[i] < place.len)
-      x[i] = *reinterpret_cast<const float4 *>(data + (place.start + row[i]) * src.row_stride +
-                                               head * src.head_stride + col);
-    big = fmaxf(big, largest(x[i]));
-  }
-  int ex = 0;
-  if (which != 0) {
-#pragma unroll
-    for (int i = 1; i < 32; i <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, i));
-    if (lane == 0) warp_big[warp] = big;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 8; ++i) big = fmaxf(big, warp_big[i]);
-    ex = exponent(big);
-    if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = ldexpf(1.0f, ex);
-  }
-#pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    if (which == 0) {
-      float b = largest(x[i]);
-#pragma unroll
-      for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
-      ex = exponent(b);
+    for (int i = 0; i < ROWS; ++i) {
+      row[i] = place.tile * kSplitRows + warp * 8 + i * (32 / LANES) + lane / LANES;
+      x[i] = make_float4(0, 0, 0, 0);
+      if (row[i] < place.len)
+        x[i] = *reinterpret_cast<const float4 *>(data + (place.start + row[i]) * src.row_stride +
+                                                 head * src.head_stride + col);
+      big = fmaxf(big, largest(x[i]));
     }
-    if (row[i] >= place.len) continue;
-    const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
-    if (which == 0 && col == 0) a.q_pow[t] = ldexpf(1.0f, ex);
-    uint2 hi, lo;
-    split4(x[i], ldexpf(1.0f, -ex), hi, lo);
-    *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
-    *reinterpret_cast<uint2 *>(a.planes[which][1] + t * D + col) = lo;
+    int ex = 0;
+    if (which != 0) {
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, i));
+      if (lane == 0) warp_big[warp] = big;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) big = fmaxf(big, warp_big[i]);
+      ex = exponent(big);
+      if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = ldexpf(1.0f, ex);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      if (which == 0) {
+        float b = largest(x[i]);
+#pragma unroll
+        for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
+        ex = exponent(b);
+      }
+      if (row[i] >= place.len) continue;
+      const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
+      if (which == 0 && col == 0) a.q_pow[t] = ldexpf(1.0f, ex);
+      uint2 hi, lo;
+      split4(x[i], ldexpf(1.0f, -ex), hi, lo);
+      *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
+      *reinterpret_cast<uint2 *>(a.planes[which][1] + t * D + col) = lo;
+    }
+    if (MANY) __syncthreads();  // warp_big
   }
 }
 
@@ -1066,17 +1081,24 @@ int launch(const Maps &maps, const Args &a, cudaStream_t s, const DevInfo &dev) 
 }
 
 template <int D>
-int launch_split(const SplitArgs &a, cudaStream_t s) {
+int launch_split(const SplitArgs &a, cudaStream_t s, const DevInfo &dev) {
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(a.tiles), static_cast<unsigned>(a.q.heads + 2 * a.k.heads), 1);
+  // A head a block, so that a tile's loads are under way at once in all of them. With more sequences than the lookup
+  // of a tile takes in a few steps, a block looks it up for several heads, in eight rounds of blocks.
+  // 4096 sequences of a row, 16 and 8 heads: the whole call 3.6 instead of 6.8 ms; 300 of them 0.30 and 0.32.
+  const bool many = a.batch > 256;
+  const int64_t heads = a.q.heads + 2 * a.k.heads, rounds = (int64_t(dev.sm_count) * 4 * 8 + a.tiles - 1) / a.tiles;
+  cfg.gridDim =
+      dim3(static_cast<unsigned>(a.tiles), static_cast<unsigned>(many ? std::min(heads, rounds) : heads), 1);
   cfg.blockDim = dim3(kSplitThreads, 1, 1);
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, attn_split_kernel<D>, a) != cudaSuccess) return WOQ_ECUDA;
+  const auto kern = many ? attn_split_kernel<D, true> : attn_split_kernel<D, false>;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return WOQ_ECUDA;
   count_launches(1);
   return WOQ_OK;
 }
@@ -1168,7 +1190,7 @@ int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, 
     sp.tokens = tokens;
     sp.tiles = a.tiles;
     sp.batch = batch;
-    const int rc = dim == 128 ? launch_split<128>(sp, s) : launch_split<64>(sp, s);
+    const int rc = dim == 128 ? launch_split<128>(sp, s, dev) : launch_split<64>(sp, s, dev);
     if (rc != WOQ_OK) return rc;
   }
   if (dim == 128)
