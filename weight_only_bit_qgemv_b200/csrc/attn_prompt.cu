@@ -947,29 +947,41 @@ struct SplitArgs {
 
 constexpr int kSplitThreads = 256;
 
-// x = hi + lo with 22 bits; what is not finite stays as it is, with nothing beside it.
-__device__ __forceinline__ void split4(float4 x, float up, uint2 &hi, uint2 &lo) {
-  const float *f = reinterpret_cast<const float *>(&x);
-  __half h[4], r[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float y = f[i] * up;
-    h[i] = __float2half_rn(y);
-    r[i] = isfinite(f[i]) ? __float2half_rn(y - __half2float(h[i])) : __float2half_rn(0.0f);
-  }
-  auto two = [](__half a, __half b) {
-    const __half2 p = __halves2half2(a, b);
-    return *reinterpret_cast<const uint32_t *>(&p);
+// x = hi + lo with 22 bits; what is not finite (`finite`: nothing) stays as it is, with nothing beside it.
+__device__ __forceinline__ void split4(float4 x, float up, bool finite, uint2 &hi, uint2 &lo) {
+  auto two = [&](float a, float b, uint32_t &h, uint32_t &l) {
+    const float2 y = __fmul2_rn(make_float2(a, b), make_float2(up, up));
+    h = pack<kF16>(y.x, y.y);
+    const float2 back = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+    float2 rest = __fadd2_rn(y, make_float2(-back.x, -back.y));
+    if (!finite) {
+      if (!isfinite(a)) rest.x = 0;
+      if (!isfinite(b)) rest.y = 0;
+    }
+    l = pack<kF16>(rest.x, rest.y);
   };
-  hi = make_uint2(two(h[0], h[1]), two(h[2], h[3]));
-  lo = make_uint2(two(r[0], r[1]), two(r[2], r[3]));
+  two(x.x, x.y, hi.x, lo.x);
+  two(x.z, x.w, hi.y, lo.y);
 }
-__device__ __forceinline__ float largest(float4 x) {  // of what is finite
+// The larger of a and the largest |x|, NaN if there is one among them.
+__device__ __forceinline__ float larger(float a, float4 x) {
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(x.x), "f"(x.y));
+  asm("max.NaN.abs.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(x.z), "f"(x.w));
+  return a;
+}
+__device__ __forceinline__ float larger(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
+__device__ __forceinline__ float largest_finite(float4 x) {
   auto f = [](float y) { return isfinite(y) ? fabsf(y) : 0.0f; };
   return fmaxf(fmaxf(f(x.x), f(x.y)), fmaxf(f(x.z), f(x.w)));
 }
-// The power of two that a largest value in [2^13, 2^14) takes.
-__device__ __forceinline__ int exponent(float big) { return big > 0 ? max(min(ilogbf(big) - 13, 113), -113) : 0; }
+// The power of two that a largest value in [2^13, 2^14) takes, within 2^+-113; 2^e for such an e.
+__device__ __forceinline__ int exponent(float big) {
+  return big > 0 ? max(min(static_cast<int>(__float_as_uint(big) >> 23) - 140, 113), -113) : 0;
+}
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Block (tile of 64 rows of a sequence, a head, or MANY of q, k and v): eight warps of eight rows, a lane four values of a
 // row.
@@ -1010,32 +1022,51 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
       if (row[i] < place.len)
         x[i] = *reinterpret_cast<const float4 *>(data + (place.start + row[i]) * src.row_stride +
                                                  head * src.head_stride + col);
-      big = fmaxf(big, largest(x[i]));
+      big = larger(big, x[i]);
     }
     int ex = 0;
+    bool finite = true;
     if (which != 0) {
+      auto of_block = [&](float b) {
 #pragma unroll
-      for (int i = 1; i < 32; i <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, i));
-      if (lane == 0) warp_big[warp] = big;
-      __syncthreads();
+        for (int i = 1; i < 32; i <<= 1) b = larger(b, __shfl_xor_sync(0xffffffffu, b, i));
+        if (lane == 0) warp_big[warp] = b;
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < 8; ++i) big = fmaxf(big, warp_big[i]);
+        for (int i = 0; i < 8; ++i) b = larger(b, warp_big[i]);
+        return b;
+      };
+      big = of_block(big);
+      finite = big < INFINITY;
+      if (!finite) {
+        __syncthreads();
+        big = 0;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) big = fmaxf(big, largest_finite(x[i]));
+        big = of_block(big);
+      }
       ex = exponent(big);
-      if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = ldexpf(1.0f, ex);
+      if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = power(ex);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       if (which == 0) {
-        float b = largest(x[i]);
+        float b = larger(0.0f, x[i]);
 #pragma unroll
-        for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
+        for (int k = 1; k < LANES; k <<= 1) b = larger(b, __shfl_xor_sync(0xffffffffu, b, k));
+        finite = __all_sync(0xffffffffu, b < INFINITY);
+        if (!finite) {
+          b = largest_finite(x[i]);
+#pragma unroll
+          for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
+        }
         ex = exponent(b);
       }
       if (row[i] >= place.len) continue;
       const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
-      if (which == 0 && col == 0) a.q_pow[t] = ldexpf(1.0f, ex);
+      if (which == 0 && col == 0) a.q_pow[t] = power(ex);
       uint2 hi, lo;
-      split4(x[i], ldexpf(1.0f, -ex), hi, lo);
+      split4(x[i], power(-ex), finite, hi, lo);
       *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
       *reinterpret_cast<uint2 *>(a.planes[which][1] + t * D + col) = lo;
     }
