@@ -6,10 +6,10 @@
 // is three shuffles among eight lanes, and a lane's four codes are one 16-bit store into the row's
 // 64 bytes. The loads of both heads' keys and values are issued before any is used.
 //
-// Measured (8 key heads, dim 128, float32, a cold L2, a launch's time included): 39,151 tokens are appended in 98 us
-// (3.7 TB/s: the quantiser's instructions, two thirds of the cycles on the integer pipe) and gathered in 80 us
-// (4.6 TB/s); 64 tokens in 3 us each. Blocks of 256 threads 101 us; a fourth block of them an SM, 64 registers, 111;
-// 4 or 16 pieces a warp instead of 8, 104 and 110.
+// Measured (8 key heads, dim 128, float32, a cold L2, a launch's time included): 39,151 tokens are appended in 93 us
+// (3.9 TB/s: the quantiser's instructions, 60 % of the cycles on the integer pipe) and gathered in 77 us (4.8 TB/s);
+// 64 tokens in 3 us each. A fourth block of 256 threads an SM, 64 registers: appending 10 % slower; 4 or 16 pieces
+// a warp instead of 8: 3 to 15 %.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -139,29 +139,46 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
   const int64_t first = (blockIdx.x * int64_t(kThreads / 32) + (threadIdx.x >> 5)) * a.per;
   const int64_t last = first + a.per < items ? first + a.per : items;
   if (first >= last) return;
-  auto load = [&](int64_t t, int h0, float4 (&x)[kHeadsPerWarp][ROWS]) {
+  int64_t t = first / a.chunks;
+  int chunk = static_cast<int>(first % a.chunks);
+  // This lane's rows: keys and values, or one of them. `at`: its values of the first head of the piece at hand, in
+  // elements, which goes on by additions.
+  woq_rows rows[ROWS];
+  int64_t at[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    rows[r] = (ROWS == 2 ? r : part) ? a.v : a.k;
+    if (F32) rows[r].dtype = WOQ_F32;
+    at[r] = t * rows[r].row_stride + chunk * kHeadsPerWarp * rows[r].head_stride + 4 * h;
+  }
+  auto load = [&](int h0, float4 (&x)[kHeadsPerWarp][ROWS]) {
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp; ++i)
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        const woq_rows &src = (ROWS == 2 ? r : part) ? a.v : a.k;
         x[i][r] = make_float4(0, 0, 0, 0);
-        if (h0 + i < a.heads)
-          x[i][r] = load4(src.data, t * src.row_stride + (h0 + i) * src.head_stride + 4 * h, F32 ? WOQ_F32 : src.dtype);
+        if (h0 + i < a.heads) x[i][r] = load4(rows[r].data, at[r] + i * rows[r].head_stride, rows[r].dtype);
       }
   };
-  int64_t t = first / a.chunks;
-  int chunk = static_cast<int>(first % a.chunks);
   float4 next[kHeadsPerWarp][ROWS];
-  if constexpr (APPEND) load(t, chunk * kHeadsPerWarp, next);
+  if constexpr (APPEND) load(chunk * kHeadsPerWarp, next);
   Place p = place_of(t, a.cu, a.start, a.batch, a.table, a.width, a.shift, a.pages);
   for (int64_t item = first; item < last; ++item) {
     const int h0 = chunk * kHeadsPerWarp;
     const int64_t token = t;
     const Place at_page = p;
+    int64_t here[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      here[r] = at[r];
+      at[r] += kHeadsPerWarp * rows[r].head_stride;
+    }
     if (++chunk == a.chunks) {
       chunk = 0;
       ++t;
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+        at[r] += rows[r].row_stride - int64_t(a.chunks) * kHeadsPerWarp * rows[r].head_stride;
     }
     float4 x[kHeadsPerWarp][ROWS];
     if constexpr (APPEND) {
@@ -169,45 +186,48 @@ __global__ void __launch_bounds__(kThreads) kv4_rows_kernel(const Args a) {
       for (int i = 0; i < kHeadsPerWarp; ++i)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) x[i][r] = next[i][r];
-      if (item + 1 < last) load(t, chunk * kHeadsPerWarp, next);
+      if (item + 1 < last) load(chunk * kHeadsPerWarp, next);
     }
     if (t != token && item + 1 < last)
       p = place_of(t, a.cu, a.start, a.batch, a.table, a.width, a.shift, a.pages);
     if (!at_page.in || (APPEND && at_page.page < 0)) continue;  // warp-uniform
-    // This lane's halfword and scale of the first head's key row; the others are whole pages of rows on.
+    // This lane's halfword and scale of the first head's rows; the others are whole pages of rows on.
     const int64_t head0 = at_page.page < 0 ? 0 : at_page.page * a.heads + h0;
-    uint16_t *codes = reinterpret_cast<uint16_t *>(a.codes) + (head0 * 2 * page + at_page.slot) * (D / 4);
-    uint16_t *scales = a.scales + (head0 * page + at_page.slot) * 2 * NB + h / 8;
     const int64_t row_step = page * (D / 4), scale_step = page * 2 * NB;
+    uint16_t *codes[ROWS], *scales[ROWS];
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const int kv = ROWS == 2 ? r : part;
+      codes[r] = reinterpret_cast<uint16_t *>(a.codes) + head0 * 2 * row_step + at_page.slot * (D / 4) +
+                 (kv ? row_step + value_halfword<D>(h) : key_halfword<D>(h));
+      scales[r] = a.scales + head0 * scale_step + at_page.slot * 2 * NB + kv * NB + h / 8;
+    }
     uint16_t sc[kHeadsPerWarp][ROWS], w[kHeadsPerWarp][ROWS];
     if constexpr (!APPEND) {
 #pragma unroll
       for (int i = 0; i < kHeadsPerWarp; ++i)
 #pragma unroll
         for (int r = 0; r < ROWS; ++r) {
-          const int kv = ROWS == 2 ? r : part;
           sc[i][r] = w[i][r] = 0;
           if (h0 + i >= a.heads || at_page.page < 0) continue;
-          w[i][r] = codes[(2 * i + kv) * row_step + (kv ? value_halfword<D>(h) : key_halfword<D>(h))];
-          sc[i][r] = scales[i * scale_step + kv * NB];
+          w[i][r] = codes[r][2 * i * row_step];
+          sc[i][r] = scales[r][i * scale_step];
         }
     }
 #pragma unroll
     for (int i = 0; i < kHeadsPerWarp; ++i) {
 #pragma unroll
       for (int r = 0; r < ROWS; ++r) {
-        const int hd = h0 + i, kv = ROWS == 2 ? r : part;
-        if (hd >= a.heads) continue;  // warp-uniform
+        if (h0 + i >= a.heads) continue;  // warp-uniform
         if constexpr (APPEND) {
           uint16_t s;
           const uint32_t c = quantise(x[i][r], &s);
-          codes[(2 * i + kv) * row_step + (kv ? value_halfword<D>(h) : key_halfword<D>(h))] = static_cast<uint16_t>(c);
-          if ((h & 7) == 0) scales[i * scale_step + kv * NB] = s;
+          codes[r][2 * i * row_step] = static_cast<uint16_t>(c);
+          if ((h & 7) == 0) scales[r][i * scale_step] = s;
         } else {
-          const woq_rows &dst = kv ? a.v : a.k;
           const float s = __half2float(__ushort_as_half(sc[i][r]));
           const int c = static_cast<int>(w[i][r]) << 16;  // sign-extend each nibble from the top
-          store4(dst.data, token * dst.row_stride + hd * dst.head_stride + 4 * h, F32 ? WOQ_F32 : dst.dtype,
+          store4(rows[r].data, here[r] + i * rows[r].head_stride, rows[r].dtype,
                  make_float4(s * static_cast<float>(c << 12 >> 28), s * static_cast<float>(c << 8 >> 28),
                              s * static_cast<float>(c << 4 >> 28), s * static_cast<float>(c >> 28)));
         }
