@@ -287,3 +287,16 @@ def test_thousands_of_sequences(dtype):
         unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
         assert ((out[i:j].double() - want).abs() <= (2 * e + 2.0**-18 + 2 * unit) * size + unit * want.abs()).all()
     assert woq.device_status() == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_thousands_of_empty_sequences(dtype):
+    """Many more blocks than tiles: what there is of rows belongs to no sequence, or to the last one."""
+    q, k, v = fused(16, 600, 4, 2, 64, dtype)
+    out = torch.full((600, 4, 64), 7.0, dtype=dtype, device="cuda")
+    woq.attn_prompt(q, k, v, torch.full((20001,), 600, dtype=torch.int32, device="cuda"), out=out)
+    assert (out == 7).all()
+    cu = torch.zeros(20001, dtype=torch.int32, device="cuda")
+    cu[-1] = 600
+    assert torch.equal(woq.attn_prompt(q, k, v, cu), woq.attn_prompt(q, k, v, ints([0, 600])))
+    assert woq.device_status() == _lib.WOQ_OK
