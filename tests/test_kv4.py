@@ -352,3 +352,20 @@ def test_no_tokens_and_interleaved_results():
     both = torch.empty(40, 2, 2, 64, device="cuda")
     woq.kv4_gather(copy.deepcopy(cache), cu, table, k_out=both[:, :, 0], v_out=both[:, :, 1])
     assert torch.equal(both[:, :, 0], k) and torch.equal(both[:, :, 1], v) and torch.equal(v, -k)
+
+
+@pytest.mark.parametrize("batch,length,kv", [(1, 2000, 8), (8, 300, 8), (32, 260, 8), (70, 200, 8), (3, 9000, 2)])
+def test_attention_over_sequences_of_one_length(batch, length, kv):
+    """Few and many sequences of one length: parts of a sequence's own, a sequence in each part, and more of both."""
+    rng = np.random.default_rng(batch)
+    page, dim = 64, 64
+    width = -(-length // page)
+    table = rng.permutation(batch * width).reshape(batch, width)
+    cache = random_cache(rng, batch * width, kv, dim, page)
+    q = torch.from_numpy(rng.standard_normal((batch, 2 * kv, dim)).astype(np.float32)).cuda()
+    ws = woq.kv4_attn_workspace(cache, q)
+    first = check_attention(cache, q, [length] * batch, table.tolist(), workspace=ws)
+    for lens in ([length - 31] * batch, [(7 * b) % length for b in range(batch)], [length] + [0] * (batch - 1)):
+        out = check_attention(cache, q, lens, table.tolist(), workspace=ws)
+        assert torch.equal(woq.kv4_attn(q, cache, ints(lens), ints(table), workspace=ws), out)
+    assert torch.equal(woq.kv4_attn(q, cache, ints([length] * batch), ints(table), workspace=ws), first)

@@ -22,7 +22,7 @@
 // The left operand of the second product is the result of the first without leaving its registers.
 //
 // Split: all sequences' tokens, in units of 32 per (sequence, key head), are one line that is cut into
-// equal parts, one for each block, whatever the lengths are: the lengths are read on the device. A part that
+// equal parts, a block's each, whatever the lengths are: the lengths are read on the device. A part that
 // covers only some of a (sequence, key head) leaves its sum, maximum and total in the workspace;
 // the last of the blocks concerned adds them in the order of the tokens (the same bits on every call).
 //
@@ -30,8 +30,8 @@
 // (three per 16 tokens: keys, values, scales are each contiguous within a page). Three blocks of four warps with
 // two units each under way keep 110 KB an SM in flight; more blocks or stages gained nothing.
 //
-// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 132 us
-// (2.3 TB/s), 4 of 100,000 to 131,072 175 us (3.0 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 70 us.
+// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 133 us
+// (2.3 TB/s), 4 of 100,000 to 131,072 173 us (3.1 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 69 us.
 // What holds it back is not the bytes but 27 instructions a token and key head, issued in 53 % of the
 // cycles: three warps a scheduler, whose registers are full, do not cover one another's latencies better.
 #include <algorithm>
