@@ -442,7 +442,8 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
  *   workspace  device, 256-byte aligned, at least kv4_attn_workspace_bytes. It must be zero before
  *           the first call, and every call leaves its counters zero (after a WOQ_ETIMEOUT from
  *           woq_device_status, zero it before reuse); its size goes by batch and heads, not by
- *           lengths. Calls (captured ones too) that share a workspace must be ordered on one stream.
+ *           lengths. One may serve calls of different shapes, if it has room for each. Calls
+ *           (captured ones too) that share a workspace must be ordered on one stream.
  * batch 1 to 4096. One launch whose grid does not depend on the lengths. Non-finite values in q, or in a
  * block of a token that is attended to, make the results they enter NaN; nothing else of the
  * cache's pages, such as slots behind the last token, has an influence.

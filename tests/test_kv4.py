@@ -369,3 +369,22 @@ def test_attention_over_sequences_of_one_length(batch, length, kv):
         out = check_attention(cache, q, lens, table.tolist(), workspace=ws)
         assert torch.equal(woq.kv4_attn(q, cache, ints(lens), ints(table), workspace=ws), out)
     assert torch.equal(woq.kv4_attn(q, cache, ints([length] * batch), ints(table), workspace=ws), first)
+
+
+def test_one_workspace_serves_calls_of_many_shapes():
+    """Sized and zeroed once for the largest call; smaller and larger ones in turn, with sequences that parts share."""
+    rng = np.random.default_rng(16)
+    caches = {dim: random_cache(rng, 64, 8, dim, 64) for dim in (64, 128)}
+    calls = []
+    for batch, group, dim in ((8, 2, 128), (16, 2, 128), (3, 16, 128), (16, 16, 64), (8, 2, 64), (3, 2, 64), (16, 16, 128)):
+        q = torch.from_numpy(rng.standard_normal((batch, 8 * group, dim)).astype(np.float32)).cuda()
+        lens = rng.integers(1, 1024, batch)
+        lens[0] = 4000
+        calls.append((q, caches[dim], ints(lens), ints(rng.integers(0, 64, (batch, 63)))))
+    want = [woq.kv4_attn(*c) for c in calls]
+    sizes = [woq.kv4_attn_workspace(c[1], c[0]).nbytes for c in calls]
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    for i in (0, 1, 2, 3, 4, 5, 6, 0, 6, 5, 3, 1, 2, 4, 0):
+        out = torch.full_like(want[i], 7.0)
+        assert torch.equal(woq.kv4_attn(*calls[i], out=out, workspace=ws), want[i]), i
+    assert woq.device_status() == _lib.WOQ_OK

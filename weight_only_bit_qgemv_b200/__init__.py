@@ -485,8 +485,8 @@ def kv4_gather(cache: KV4Cache, cu: torch.Tensor, table: torch.Tensor, start: to
 
 
 def kv4_attn_workspace(cache: KV4Cache, q: torch.Tensor) -> torch.Tensor:
-    """A zeroed workspace for kv4_attn calls with queries shaped like ``q`` (every call leaves its
-    counters zero; calls that share one must be ordered on one stream)."""
+    """A zeroed workspace for kv4_attn calls with queries shaped like ``q``, and for smaller ones (every call
+    leaves its counters zero; calls that share one must be ordered on one stream)."""
     need = _lib.lib().kv4_attn_workspace_bytes(cache.desc(), q.shape[1], q.shape[0])
     return torch.zeros(int(need), dtype=torch.uint8, device=cache.codes.device)
 

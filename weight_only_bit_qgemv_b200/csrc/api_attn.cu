@@ -123,7 +123,7 @@ size_t kv4_attn_workspace_bytes(const woq_kv4 *cache, int32_t q_heads, int32_t b
   if (q_heads < 1 || q_heads % cache->kv_heads || q_heads / cache->kv_heads > woq::kMaxGroup) return 0;
   DevInfo dev;
   const int sms = woq::current_device(&dev) == WOQ_OK ? dev.sm_count : 148;
-  return woq::kv4_attn_workspace(batch, cache->kv_heads, q_heads / cache->kv_heads, cache->dim, sms);
+  return woq::kv4_attn_workspace(batch, cache->kv_heads, q_heads / cache->kv_heads, sms);
 }
 
 int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32_t batch, const int32_t *table,
@@ -144,7 +144,7 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
   if (woq::overlap(*q, *o, batch, cache->dim)) return WOQ_EINVAL;
   DevInfo dev;
   rc = woq::current_device(&dev);
-  const size_t need = woq::kv4_attn_workspace(batch, cache->kv_heads, q->heads / cache->kv_heads, cache->dim,
+  const size_t need = woq::kv4_attn_workspace(batch, cache->kv_heads, q->heads / cache->kv_heads,
                                               rc == WOQ_OK ? dev.sm_count : 148);
   if (!workspace || workspace_bytes < need) return WOQ_EWORKSPACE;
   if (!woq::aligned(workspace, 256)) return WOQ_EALIGN;

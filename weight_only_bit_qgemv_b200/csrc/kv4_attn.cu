@@ -719,16 +719,18 @@ int launch(const Args &a, cudaStream_t s, const DevInfo &dev) {
   return WOQ_OK;
 }
 
-size_t counters_bytes(int32_t batch, int32_t kv_heads, int32_t group) {
-  const size_t n = static_cast<size_t>(batch) * kv_heads * ((group + kHeads - 1) / kHeads) * 4;
-  return (n + 255) & ~static_cast<size_t>(255);
+// The workspace: partial results, of the larger dim's size whatever the call's, and then the counters. So no call's
+// partial results lie where another's counters are, and one workspace serves calls of all shapes that it has room for.
+size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }
+
+size_t partials_bytes(int sm_count) {
+  return up256(static_cast<size_t>(sm_count) * kBlocksPerSm * 2 * Shape<128>::Slot * sizeof(float));
 }
 
 }  // namespace
 
-size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int32_t dim, int sm_count) {
-  const size_t slot = (dim == 128 ? Shape<128>::Slot : Shape<64>::Slot) * sizeof(float);
-  return counters_bytes(batch, kv_heads, group) + static_cast<size_t>(sm_count) * kBlocksPerSm * 2 * slot;
+size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int sm_count) {
+  return partials_bytes(sm_count) + up256(static_cast<size_t>(batch) * kv_heads * ((group + kHeads - 1) / kHeads) * 4);
 }
 
 int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, int32_t batch, const int32_t *table,
@@ -749,9 +751,8 @@ int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, in
   a.group = q.heads / c.kv_heads;
   a.chunks = (a.group + kHeads - 1) / kHeads;
   a.scale = scale * 1.44269504088896340736f;
-  a.counters = static_cast<unsigned *>(workspace);
-  a.partials = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) +
-                                         counters_bytes(batch, c.kv_heads, a.group));
+  a.partials = static_cast<float *>(workspace);
+  a.counters = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) + partials_bytes(dev.sm_count));
   const long long lim = wait_limit_cycles();
   a.wait_limit = lim > 0 ? lim : kWaitLimit;
   return c.dim == 128 ? launch<128>(a, s, dev) : launch<64>(a, s, dev);

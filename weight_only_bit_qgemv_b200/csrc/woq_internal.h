@@ -83,7 +83,7 @@ int launch_kv4_rows(const woq_kv4 &c, const woq_rows &k, const woq_rows &v, int6
 
 // ---- kv4_attn.cu ----
 constexpr int kKv4MaxBatch = 4096;  // the kernel keeps a prefix sum over the sequences in shared memory
-size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int32_t dim, int sm_count);
+size_t kv4_attn_workspace(int32_t batch, int32_t kv_heads, int32_t group, int sm_count);
 int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, int32_t batch, const int32_t *table,
                     int64_t width, float scale, const woq_rows &o, void *workspace, cudaStream_t s,
                     const DevInfo &dev);
