@@ -429,8 +429,9 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
 /*
  * kv4_attn -- a decode step's attention: for each sequence b and query head h, with key head
  * h / (q.heads / kv_heads), o[b, h] = sum_j p_j v_j over the sequence's lens[b] cached tokens,
- * p = softmax_j(scale * q[b, h] . k_j). FP32 accuracy: the codes are exact, q and p enter the
- * tensor cores with 22 significant bits, and each block's FP32 sum is scaled once.
+ * p = softmax_j(scale * q[b, h] . k_j). FP32 accuracy, whatever the scales' sizes: the codes are
+ * exact, q and p times a value's scale enter the tensor cores with 22 significant bits, and each
+ * block's FP32 sum is scaled once.
  * Deterministic for the same arguments on the same device.
  *   q       device, [batch, q.heads, dim]; q.heads a multiple of kv_heads, at most 64 a key head
  *   lens    device, int32 [batch]: cached tokens, the new one among them if it attends to itself.

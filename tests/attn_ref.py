@@ -75,3 +75,26 @@ def tolerance(ref, size, dtype, products=22):
     e = 2.0 ** (2 - products) * size[..., :1]
     unit = 0.0 if dtype == torch.float32 else UNIT[dtype]
     return (2 * e + 2.0 ** (3 - products)) * size[..., 1:] + unit * np.abs(ref) + 1e-30
+
+
+def attend_by_column(q, k, v, scale):
+    """attend() for q [heads, dim] over k, v [tokens, kv_heads, dim], and what bounds its error column by column: per head
+    the largest sum_d |q_d k_d| scale of a token, and per column sum_j p_j times the largest |v_j| of its 32 columns."""
+    out, size = attend(q, k, v, scale)
+    heads, kv, dim = q.shape[0], k.shape[1], q.shape[1]
+    big = np.repeat(np.abs(v).reshape(*v.shape[:2], dim // 32, 32).max(-1), 32, axis=-1)
+    col = np.zeros(q.shape)
+    for h in range(heads):
+        x = k[:, h * kv // heads] @ q[h] * scale
+        p = np.exp(x - x.max())
+        col[h] = p @ big[:, h * kv // heads] / p.sum()
+    return out, size[:, :1], col
+
+
+def tolerance_by_column(ref, e, col, dtype):
+    """tolerance() with the weighted mean of the values' sizes for the largest of them. Scores as there: E = 2^-20 sum
+    |q k| scale, 2 E of every weight. Weights' exponentials and splits and the products with the scales are off by
+    2^-22 of each term, three times; the split's last step is 2^-25 of a unit's largest term at most for each of 32
+    tokens, 2^-20; FP32 additions of a few units 2^-21: less than 2^-18 of the sum of all terms' sizes."""
+    unit = 0.0 if dtype == torch.float32 else UNIT[dtype]
+    return (2.0**-19 * e + 2.0**-18) * col + unit * np.abs(ref) + 1e-30

@@ -388,3 +388,93 @@ def test_one_workspace_serves_calls_of_many_shapes():
         out = torch.full_like(want[i], 7.0)
         assert torch.equal(woq.kv4_attn(*calls[i], out=out, workspace=ws), want[i]), i
     assert woq.device_status() == _lib.WOQ_OK
+
+
+def check_columns(cache, q, n, table, **kw):
+    """One sequence's attention, with a tolerance by column: a token far above the others counts by its weight."""
+    out = woq.kv4_attn(q, cache, ints([n]), ints([table]), **kw)
+    k, v = ref.read_pages(cache.codes, cache.scales)
+    at = [(table[j // cache.page], j % cache.page) for j in range(n)]
+    kb, vb = (np.array([x[p, :, s] for p, s in at]) for x in (k, v))
+    want, e, col = ref.attend_by_column(q[0].double().cpu().numpy(), kb, vb, cache.dim**-0.5)
+    err = np.abs(out[0].double().cpu().numpy() - want)
+    assert (err <= ref.tolerance_by_column(want, e, col, q.dtype)).all(), (err.max(), (err / (col + 1e-300)).max())
+    assert woq.device_status() == _lib.WOQ_OK
+
+
+def plain_cache(rng, pages, heads, dim, page):
+    """Scales as kv4_append writes them of normal values."""
+    cache = random_cache(rng, pages, heads, dim, page)
+    s = np.abs(2.0 + 0.4 * rng.standard_normal(tuple(cache.scales.shape))) / 7
+    cache.scales.copy_(torch.from_numpy(s.astype(np.float16)))
+    return cache
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("score", [0.0, -6.0, -40.0])
+@pytest.mark.parametrize("big", [8.0, 1024.0, 60000.0])
+@pytest.mark.parametrize("at", [0, 150, 310])
+def test_attention_a_value_far_above_the_others(dim, score, big, at):
+    """One token's values are far above the others', in all blocks or in one, whatever its weight."""
+    rng = np.random.default_rng(at)
+    cache = plain_cache(rng, 20, 1, dim, 16)
+    q = torch.from_numpy((0.2 + rng.random((1, 8, dim))).astype(np.float32)).cuda()
+    # the token's key: codes -1, scales that bring its scores to about `score`
+    cache.codes[at // 16, 0, 0, at % 16] = 0xFF
+    cache.scales[at // 16, 0, at % 16, 0] = -score / (0.7 * dim**0.5)
+    for blocks in (slice(None), slice(1, 2)):
+        cache.scales[at // 16, 0, at % 16, 1, blocks] = big
+        check_columns(cache, q, 311, list(range(20)))
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_attention_value_blocks_and_tokens_of_different_sizes(dim):
+    rng = np.random.default_rng(18)
+    nb, table = dim // 32, list(range(20))
+    q = torch.from_numpy(rng.standard_normal((1, 8, dim)).astype(np.float32)).cuda()
+    every = torch.arange(16, device="cuda")
+    for low in (2.0**-8, 2.0**-12, 2.0**-15, 2.0**-20):
+        for high in (1.0, 64.0, 30000.0):
+            cache = plain_cache(rng, 20, 1, dim, 16)
+            cache.scales[..., 1, 0] = low                       # one block of all tokens
+            cache.scales[..., 1, nb - 1] = high
+            check_columns(cache, q, 320, table)
+            cache = plain_cache(rng, 20, 1, dim, 16)
+            cache.scales[:, :, every % 3 == 0, 1] = low         # tokens in turn
+            cache.scales[:, :, every % 3 == 1, 1] = high
+            check_columns(cache, q, 320, table)
+            cache.scales[:10, :, :, 1] = low                    # one part of the context, then the other
+            cache.scales[10:, :, :, 1] = high
+            check_columns(cache, q, 320, table)
+            cache.scales[10:, :, 3, 1] = 0                      # and blocks of zeros
+            check_columns(cache, q, 320, table)
+            cache.scales[:10, :, :, 1] = high
+            cache.scales[10:, :, :, 1] = low
+            check_columns(cache, q, 320, table)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("gap", [5.0, 12.0, 25.0])
+def test_attention_a_token_with_the_weight_and_small_values(dim, gap):
+    """The first token has nearly all the weight and tiny values, or none: the others' small weights make the result."""
+    rng = np.random.default_rng(19)
+    for size in (0.5, 1e-3, 2.0**-22, 0.0):
+        cache = plain_cache(rng, 70, 1, dim, 16)
+        q = torch.from_numpy((0.2 + rng.random((1, 8, dim))).astype(np.float32)).cuda()
+        cache.codes[0, 0, 0, 0] = 0x11
+        cache.scales[0, 0, 0, 0] = gap / (0.7 * dim**0.5) + 1
+        cache.scales[0, 0, 0, 1] = size
+        cache.scales[:, :, :, 0] *= 0.1
+        cache.scales[0, 0, 0, 0] *= 10
+        check_columns(cache, q, 1111, list(range(70)))
+
+
+def test_attention_turns_from_values_of_one_size_to_another_and_back():
+    """Long stretches of large and of tiny values in turn, between which the scores fall and rise by tens."""
+    rng = np.random.default_rng(20)
+    cache = plain_cache(rng, 128, 2, 128, 64)
+    for i in range(128):
+        cache.scales[i, :, :, 1] *= (2.0**-14, 1.0, 2.0**12, 2.0**-8, 2.0**14)[i // 7 % 5]
+        cache.scales[i, :, :, 0] *= (1.0, 0.25, 2.0)[i // 11 % 3]
+    q = torch.from_numpy((3 * rng.standard_normal((1, 6, 128))).astype(np.float32)).cuda()
+    check_columns(cache, q, 8190, list(range(128)))

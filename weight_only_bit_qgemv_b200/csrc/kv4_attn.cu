@@ -11,7 +11,9 @@
 //
 // FP32 accuracy: the 16 rows of the left operand are 8 query heads' high binary16 parts and the
 // same heads' low parts, so that 22 bits of q, and then of p_j * vs[j, block], take part. The
-// query is scaled by a power of two into binary16's range, the value scales likewise (see `room`). Per
+// query is scaled by a power of two into binary16's range, the value scales likewise (see `room`) where
+// those of 32 tokens lie within 2^13 of one another. Where they do not, or some are 0, the products p_j * vs[j, block]
+// are made in FP32, and each head and block gets a power of two of its own. Per
 // block of 32 the key scale multiplies an FP32 block sum. Sums inside the matrix instructions, which cut
 // off what lies below their last bit, run over 32 tokens; from there on they are FP32 additions,
 // rounded to nearest. (A masked nibble is a binary16 as it stands, the subnormal u * 2^-24, and the offset
@@ -30,8 +32,8 @@
 // (three per 16 tokens: keys, values, scales are each contiguous within a page). Three blocks of four warps with
 // two units each under way keep 110 KB an SM in flight; more blocks or stages gained nothing.
 //
-// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 133 us
-// (2.3 TB/s), 4 of 100,000 to 131,072 173 us (3.1 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 69 us.
+// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 131 us
+// (2.3 TB/s), 4 of 100,000 to 131,072 174 us (3.1 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 69 us.
 // What holds it back is not the bytes but 27 instructions a token and key head, issued in 53 % of the
 // cycles: three warps a scheduler, whose registers are full, do not cover one another's latencies better.
 #include <algorithm>
@@ -53,6 +55,8 @@ constexpr int kBlocksPerSm = 3;
 constexpr int kUnit = 32;      // tokens of a unit
 constexpr int kStages = 2;     // units in a warp's ring
 constexpr int kHeads = 8;      // query heads of a pass: half the rows of a matrix instruction
+constexpr int kTop = 14;       // weights reach 2^14, which binary16 holds
+constexpr int kFall = 40;      // how far a unit's reference may be below the largest one so far, as a power of two
 constexpr int kMoreUnits = 8;  // units that a part may have more so that parts begin and end with their sequences
 constexpr long long kWaitLimit = 1LL << 32;  // cycles (~2 s)
 
@@ -124,6 +128,11 @@ __device__ __forceinline__ uint32_t high(uint32_t w, const Magic &m) {
   asm("lop3.b32 %0, %1, 0x00f000f0, %2, 0x6a;" : "=r"(u) : "r"(w), "r"(m.high));
   return u32(__hsub2(h2(u), h2(m.high)));
 }
+
+// 2^e as binary16, as its bits, where it has it: from its smallest number on to infinity.
+__device__ __forceinline__ int half_bits(int e) { return e < -24 ? 1 : e < -14 ? 1 << (e + 24) : min(e + 15, 31) << 10; }
+// The exponent of the binary16 number with these bits (neither 0 nor negative).
+__device__ __forceinline__ int half_exponent(int bits) { return bits < 0x400 ? 7 - __clz(bits) : (bits >> 10) - 15; }
 
 // a and b as binary16 high parts and binary16 remainders: 22 bits of each.
 __device__ __forceinline__ void split(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -343,13 +352,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 
     const float f = fac[g];
 
-    float m = -INFINITY;  // running maximum of the scores (log2), shared by the quad
-    float l = 0;          // this lane's sum of p
-    // p is taken times 2^6 and the value scales times 2^room: p * vs then reaches at least 1, so that
-    // binary16's smallest step is below 2^-24 of the largest. The first cancels in o / sum(p).
+    // Weights are p = 2^(score - m), at most 2^kTop. m is the unit's own largest score, so that a unit's weights keep
+    // their bits after a token that had far more weight; it changes by whole powers of two, which are exact.
+    float m = -INFINITY;
+    float highest = -INFINITY;  // the largest m so far: m is at most 2^kFall below it, which keeps sums finite
+    float l = 0;                // this lane's sum of p
+    // Value scales are taken times 2^room, so that they are in [2^-12, 2) as a rule: a block's p * vs then reaches 2 at
+    // least, and of each token binary16 cuts off at most 2^-25 (p) and 2^-26 (p * vs) of that.
     int room = 0;
-    float most = 0;  // the largest scale that room allows
-    int limit = -1;  // its bits as binary16
+    uint32_t lowest = 0xf400f400u;  // twice the bits of 2^(-12 - room), negative
+    int width = 0x33ff;             // from there on, the bits that are below those of 2^(1 - room)
     float2 acc[NB][4];  // value block, n-tile: columns of tokens' head g, dims 32 b + 8 t + i and + 4
 #pragma unroll
     for (int i = 0; i < NB; ++i)
@@ -421,6 +433,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         }
       }
       if (!full) {  // warp-uniform: tokens that are not there weigh nothing, whatever the stage holds
+        const uint32_t from = ((0u - lowest) & 0xffffu) * 0x00010001u;  // scales that need no look
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -430,13 +443,81 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
               if (!(pages_ok >> h & 1) || 16 * h + token_of(i, t, j) >= rest) {
                 (j ? s[h][i].y : s[h][i].x) = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < NB / 2; ++k) vs[h][i][j][k] = 0;
+                for (int k = 0; k < NB / 2; ++k) vs[h][i][j][k] = from;
               }
       }
 
+      // ---- softmax over the unit: weights in the scores' place, `al` for what was summed before ----
+      float shift = 0;  // change of room
+      float2 al;
+      auto softmax = [&] {
+        float mx = fmaxf(fmaxf(fmaxf(s[0][0].x, s[0][0].y), fmaxf(s[0][1].x, s[0][1].y)),
+                         fmaxf(fmaxf(s[1][0].x, s[1][0].y), fmaxf(s[1][1].x, s[1][1].y)));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // Any token makes the maximum finite, so that -infinity means that there was none: a row of
+        // scores that are all NaN or -infinity gives NaN, as the formula does.
+        mx *= f;  // a power of two: exact
+        if (pages_ok) mx = fmaxf(mx, -3.402823466e38f);
+        // rounded up: the largest weight is never above 2^kTop
+        const float own = __fadd_ru(ceilf(mx), -static_cast<float>(kTop));
+        highest = fmaxf(highest, own);
+        const float m2 = fmaxf(own, highest - static_cast<float>(kFall));
+        const float ref = m2 == -INFINITY ? 0.0f : -m2;
+        const float beta = m == -INFINITY ? -INFINITY : m - m2;
+        const float alpha = ex2(beta + shift);
+        al = make_float2(alpha, alpha);
+        l *= ex2(beta);
+        m = m2;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 y = __ffma2_rn(s[h][i], make_float2(f, f), make_float2(ref, ref));
+            s[h][i] = make_float2(ex2(y.x), ex2(y.y));
+          }
+        const float2 sum = __fadd2_rn(__fadd2_rn(s[0][0], s[0][1]), __fadd2_rn(s[1][0], s[1][1]));
+        l += sum.x + sum.y;
+      };
+
+      // ---- values ----
+      // operand(kp, kb, p): the weights times block k's scales, as sums of two binary16 numbers, and what the
+      // products with them are to be multiplied with
+      auto values = [&](auto operand) {
+#pragma unroll
+        for (int kp = 0; kp < NB / 2; ++kp) {  // pairs of blocks: one word of a lane's codes
+          uint32_t v[2][2][2];  // half, matrix, block of the pair: two tokens' four codes
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint8_t *vr = base + S::Values + 16 * h * S::RowBytes + g * (2 * NB) + kp * 4;
+              const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 0) * S::RowBytes);
+              const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 1) * S::RowBytes);
+              v[h][i][0] = __byte_perm(w0, w1, 0x5410);
+              v[h][i][1] = __byte_perm(w0, w1, 0x7632);
+            }
+#pragma unroll
+          for (int kb = 0; kb < 2; ++kb) {
+            const int k = 2 * kp + kb;
+            uint4 p[2];
+            const auto back = operand(kp, kb, p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float c[4];
+              const int sh = 8 * (i >> 1);
+              auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh, magic) : low(w >> sh, magic); };
+              mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), magic.zero);
+              mma(c, p[1], pick(v[1][0][kb]), pick(v[1][1][kb]), c);
+              acc[k][i] =
+                  __ffma2_rn(acc[k][i], al, back(__fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3]))));
+            }
+          }
+        }
+      };
+
       // ---- value scales: keep p * vs inside binary16 ----
-      // Compared as 16-bit numbers, which order binary16 of one sign; a negative scale (kv4_append
-      // writes none) counts as large and only takes the longer way.
+      // Their bits order them as 16-bit numbers. A scale of 0 or below counts as outside, and only takes a look.
       uint32_t big = 0;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
@@ -445,10 +526,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
-            for (int k = 0; k < NB / 2; ++k) big = __vmaxu2(big, vs[h][i][j][k]);
-      float shift = 0;  // change of room
-      if (__any_sync(0xffffffffu, static_cast<int>(max(big & 0xffffu, big >> 16)) > limit)) {
-        __half2 m2 = __float2half2_rn(0);
+            for (int k = 0; k < NB / 2; ++k) big = __viaddmax_u16x2(vs[h][i][j][k], lowest, big);
+      if (__any_sync(0xffffffffu, static_cast<int>(max(big & 0xffffu, big >> 16)) > width)) {
+        uint32_t most = 0, least = 0xffffffffu, zero = 0;  // sizes; less one, least and most: 0 is the most then
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -456,19 +536,56 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
-              for (int k = 0; k < NB / 2; ++k) m2 = __hmax2(m2, __habs2(h2(vs[h][i][j][k])));
-        float all = fmaxf(__low2float(m2), __high2float(m2));
+              for (int k = 0; k < NB / 2; ++k) {
+                const uint32_t size = vs[h][i][j][k] & 0x7fff7fffu;
+                most = __vmaxu2(most, size);
+                least = __vminu2(least, __vsub2(size, 0x00010001u));
+                zero = __vmaxu2(zero, __vsub2(size, 0x00010001u));
+              }
+        const int hi = __reduce_max_sync(0xffffffffu, max(most & 0xffffu, most >> 16));
+        const int lo = __reduce_min_sync(0xffffffffu, min(least & 0xffffu, least >> 16)) + 1;
+        if (hi > 0) {
+          // What room has to be for the largest and for the least.
+          const int r_max = -half_exponent(hi), r_min = -12 - half_exponent(lo);
+          const bool zeros = __any_sync(0xffffffffu, max(zero & 0xffffu, zero >> 16) == 0xffffu);
+          const bool wide = hi >= 0x7c00 || r_min > r_max || zeros;  // further apart than that, or some are 0
+          if (wide || room < r_min || room > r_max) {
+            const int next = wide || (r_min <= 0 && r_max >= 0) ? 0 : (r_min + r_max) >> 1;
+            shift = static_cast<float>(next - room);
+            room = next;
+            const int from = half_bits(-12 - room);
+            lowest = static_cast<uint32_t>(0x10000 - from) * 0x00010001u;
+            width = half_bits(1 - room) - 1 - from;
+          }
+          if (wide) {  // all of it here, so that the other way stays one piece
+            softmax();
+            // The products in FP32, times the power of two that brings a head's largest into [2^13, 2^14).
+            values([&](int kp, int kb, uint4 (&p)[2]) {
+              float2 x[2][2];
+              float top = 0;
 #pragma unroll
-        for (int i = 1; i < 32; i <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, i));
-        if (limit < 0 || all > most) {
-          // Scales from 2^-6 to 2^4 are taken as they are, others times a power of two that brings the
-          // largest to [1, 2); they may grow to 2^8 before this changes again.
-          const int ex = all > 0 && all < INFINITY ? ilogbf(all) : 0;
-          const int next = ex < -6 || ex > 3 ? -ex : 0;
-          shift = static_cast<float>(next - room);
-          room = next;
-          most = ldexpf(1.0f, 8 - next);
-          limit = __half_as_ushort(__float2half_rz(fminf(most, 65504.0f)));
+              for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const __half2 s0 = h2(vs[h][i][0][kp]), s1 = h2(vs[h][i][1][kp]);
+                  x[h][i] = make_float2(s[h][i].x * (kb ? __high2float(s0) : __low2float(s0)),
+                                        s[h][i].y * (kb ? __high2float(s1) : __low2float(s1)));
+                  top = fmaxf(top, fmaxf(fabsf(x[h][i].x), fabsf(x[h][i].y)));
+                }
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+              const int up = min(max(140 - static_cast<int>(__float_as_uint(top) >> 23), -100), 100);
+              const float u = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+              const float down = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                split(x[h][0].x * u, x[h][0].y * u, p[h].x, p[h].y);
+                split(x[h][1].x * u, x[h][1].y * u, p[h].z, p[h].w);
+              }
+              return [down](float2 c) { return __fmul2_rn(c, make_float2(down, down)); };
+            });
+            goto summed;
+          }
         }
       }
       if (room != 0) {  // warp-uniform
@@ -486,55 +603,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
                 vs[h][i][j][k] = u32(__hmul2(__hmul2(h2(vs[h][i][j][k]), a1), a2));
       }
 
-      // ---- softmax over the unit ----
-      float mx = fmaxf(fmaxf(fmaxf(s[0][0].x, s[0][0].y), fmaxf(s[0][1].x, s[0][1].y)),
-                       fmaxf(fmaxf(s[1][0].x, s[1][0].y), fmaxf(s[1][1].x, s[1][1].y)));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      // Any token makes the maximum finite, so that -infinity means that there was none: a row of
-      // scores that are all NaN or -infinity gives NaN, as the formula does.
-      mx *= f;
-      if (pages_ok) mx = fmaxf(mx, -3.402823466e38f);
-      const float m2 = fmaxf(m, mx);
-      const float ref = 6.0f - (m2 == -INFINITY ? 0.0f : m2);
-      const float beta = m == -INFINITY ? -INFINITY : m - m2;
-      const float alpha = ex2(beta + shift);
-      l *= ex2(beta);
-      m = m2;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float2 y = __ffma2_rn(s[h][i], make_float2(f, f), make_float2(ref, ref));
-          s[h][i] = make_float2(ex2(y.x), ex2(y.y));
-        }
-      const float2 sum = __fadd2_rn(__fadd2_rn(s[0][0], s[0][1]), __fadd2_rn(s[1][0], s[1][1]));
-      l += sum.x + sum.y;
-
-      // ---- values ----
-      const float2 al = make_float2(alpha, alpha);
-      uint32_t ph[2][2], pl[2][2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) split(s[h][i].x, s[h][i].y, ph[h][i], pl[h][i]);
-#pragma unroll
-      for (int kp = 0; kp < NB / 2; ++kp) {  // pairs of blocks: one word of a lane's codes
-        uint32_t v[2][2][2];  // half, matrix, block of the pair: two tokens' four codes
+      {
+        softmax();
+        uint32_t ph[2][2], pl[2][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint8_t *vr = base + S::Values + 16 * h * S::RowBytes + g * (2 * NB) + kp * 4;
-            const uint32_t w0 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 0) * S::RowBytes);
-            const uint32_t w1 = *reinterpret_cast<const uint32_t *>(vr + token_of(i, t, 1) * S::RowBytes);
-            v[h][i][0] = __byte_perm(w0, w1, 0x5410);
-            v[h][i][1] = __byte_perm(w0, w1, 0x7632);
-          }
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const int k = 2 * kp + kb;
-          uint4 p[2];
+          for (int i = 0; i < 2; ++i) split(s[h][i].x, s[h][i].y, ph[h][i], pl[h][i]);
+        values([&](int kp, int kb, uint4 (&p)[2]) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             // (ph + pl) * vs as a sum of two binary16 again: the product's rounding error is itself a
@@ -549,18 +625,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
             }
             p[h] = make_uint4(x[0], y[0], x[1], y[1]);
           }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float c[4];
-            const int sh = 8 * (i >> 1);
-            auto pick = [&](uint32_t w) { return i & 1 ? high(w >> sh, magic) : low(w >> sh, magic); };
-            mma(c, p[0], pick(v[0][0][kb]), pick(v[0][1][kb]), magic.zero);
-            mma(c, p[1], pick(v[1][0][kb]), pick(v[1][1][kb]), c);
-            acc[k][i] = __ffma2_rn(acc[k][i], al, __fadd2_rn(make_float2(c[0], c[1]), make_float2(c[2], c[3])));
-          }
-        }
+          return [](float2 c) { return c; };
+        });
       }
 
+    summed:
       __syncwarp();  // every lane has read the stage
       issue(u + kStages * kWarps, st, next);
       next = entry(u + (kStages + 1) * kWarps);
