@@ -300,3 +300,27 @@ def test_thousands_of_empty_sequences(dtype):
     cu[-1] = 600
     assert torch.equal(woq.attn_prompt(q, k, v, cu), woq.attn_prompt(q, k, v, ints([0, 600])))
     assert woq.device_status() == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("size", [2.0**20, 2.0**25, 2.0**27, 2.0**30, -(2.0**25), -(2.0**28), -(2.0**30)])
+def test_scores_far_from_zero(dtype, size):
+    """Scores that are exact whole numbers times `size`: equal ones share the weight, others have none of it."""
+    n, dim = 300, 64
+    g = torch.Generator().manual_seed(3)
+    a = torch.randint(1, 4, (n,), generator=g).cuda()
+    q = torch.zeros(n, 1, dim, device="cuda")
+    k = torch.zeros(n, 1, dim, device="cuda")
+    half = 2.0 ** round(np.log2(abs(size)) / 2)
+    q[:, 0, 3:5], k[:, 0, 3:5] = half, a[:, None] * (size / half / 2)  # two halves: binary16 has no 3 * 2^15
+    k[:100, 0, 3:5] = size / half / 2  # the first 100 are all the same
+    v = torch.randn(n, 1, dim, generator=g).cuda()
+    q, k, v = (x.to(dtype) for x in (q, k, v))
+    out = woq.attn_prompt(q, k, v, ints([0, n]), scale=1.0).double()
+    x = torch.tril(torch.ones(n, n, dtype=torch.float64, device="cuda")).log() + k[:, 0, 3].double() * 2 * half
+    p = torch.softmax(x, -1)
+    want, col = p @ v[:, 0].double(), p @ v[:, 0].double().abs()
+    # exact()'s tolerance without the scores', which are exact
+    unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
+    assert ((out[:, 0] - want).abs() <= (2.0**-18 + 2 * unit) * col + unit * want.abs()).all()
+    assert woq.device_status() == _lib.WOQ_OK

@@ -478,3 +478,24 @@ def test_attention_turns_from_values_of_one_size_to_another_and_back():
         cache.scales[i, :, :, 0] *= (1.0, 0.25, 2.0)[i // 11 % 3]
     q = torch.from_numpy((3 * rng.standard_normal((1, 6, 128))).astype(np.float32)).cuda()
     check_columns(cache, q, 8190, list(range(128)))
+
+
+@pytest.mark.parametrize("size", [2.0**20, 2.0**25, 2.0**27, 2.0**30, -(2.0**25), -(2.0**28), -(2.0**30)])
+def test_attention_scores_far_from_zero(size):
+    """Scores that are exact whole numbers times `size`: equal ones share the weight, others have none of it."""
+    rng = np.random.default_rng(22)
+    cache = plain_cache(rng, 20, 1, 64, 16)
+    cache.codes[:, :, 0] = 0x11
+    cache.scales[:, :, :, 0] = torch.from_numpy(rng.integers(1, 4, (20, 1, 16, 2)).astype(np.float16)).cuda()
+    cache.scales[:7, :, :, 0] = 2.0
+    cache.scales[:, :, :, 0, 1:] = 0
+    q = torch.zeros(1, 2, 64, device="cuda")
+    q[0, :, 5] = size
+    out = woq.kv4_attn(q, cache, ints([320]), ints([list(range(20))]), scale=1.0)[0].double().cpu().numpy()
+    k, v = ref.read_pages(cache.codes, cache.scales)
+    x = k[:, 0, :, 5].reshape(-1) * size
+    p = np.exp(x - x.max())
+    p /= p.sum()
+    v = v[:, 0].reshape(-1, 64)
+    big = np.repeat(np.abs(v).reshape(-1, 2, 32).max(-1), 32, axis=-1)
+    assert (np.abs(out - p @ v) <= ref.tolerance_by_column(p @ v, 0.0, p @ big, q.dtype)).all()
