@@ -411,9 +411,10 @@ int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, in
  *   scale   positive and finite, usually dim^-1/2
  *   workspace  device, 256-byte aligned, attn_prompt_workspace_bytes(...) bytes (0 for 16-bit types);
  *           its contents on entry do not matter; calls that share one must be ordered on one stream
- * float32: q, k and v as two binary16 planes each, 22 significant bits of every value within 2^17 of the
- * largest of its row (q) or of its 64 tokens of one head (k, v), three products on the tcgen05 tensor cores, FP32
- * sums. 16-bit: operands as they are, weights rounded to the type. The lengths stay on the device; the grid
+ * float32: q, k and v as two binary16 planes each: 22 significant bits of every value within 2^7 of the
+ * largest of its token and head, the others to 2^-28 of that largest, whatever other tokens' sizes are; weights
+ * likewise, 22 bits within 2^16 of the row's largest and the others to 2^-38 of it; three products on the tcgen05
+ * tensor cores, FP32 sums. 16-bit: operands as they are, weights rounded to the type. The lengths stay on the device; the grid
  * goes by tokens and batch. Deterministic. A value that is not finite enters only rows that see it: a
  * row that sees such a q or k is NaN, one that sees such a v is not finite in its column.
  * batch 1 to 65536; (tokens / 256 + batch) * q.heads < 2^31; tokens == 0 does nothing.

@@ -324,3 +324,79 @@ def test_scores_far_from_zero(dtype, size):
     unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
     assert ((out[:, 0] - want).abs() <= (2.0**-18 + 2 * unit) * col + unit * want.abs()).all()
     assert woq.device_status() == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("size", [1e6, 1e12, 1e30])
+@pytest.mark.parametrize("at", [0, 1, 40, 63, 64, 100])
+def test_rows_before_a_far_larger_one_keep_their_precision(dim, size, at):
+    """float32: a key's or value's size has no influence on the rows before it, and none on the keys and values beside."""
+    cu = [3, 3 + 150, 3 + 150 + 70]
+    q, k, v = fused(17, cu[-1], 4, 2, dim, torch.float32)
+    v2 = v.clone()
+    v2[3 + at] *= size
+    check(q, k, v2, cu)
+    v2[3 + at, 0] = v[3 + at, 0]
+    v2[3 + at, 0, 5] = size
+    # the columns beside the large one are bounded by it from that row on, as by one value of 22 bits
+    out = woq.attn_prompt(q, k, v2, ints(cu))
+    want, tol = exact(q, k, v2, cu, dim**-0.5)
+    tol[3 + at:cu[1], :2] += 2.0**-36 * size
+    assert ((out.double() - want).abs() <= tol).all()
+    k2 = k.clone()
+    k2[3 + at] *= size
+    if size < 1e30:  # the scores of the rows that see it are beyond 32 bits otherwise
+        check(q, k2, v, cu)
+        check(q, k2, v2, [3, 3 + at, 3 + at, cu[1], cu[2]][(at == 0):])
+    else:
+        out = woq.attn_prompt(q, k2, v, ints(cu))
+        want, tol = exact(q, k, v, cu, dim**-0.5)
+        assert ((out.double() - want).abs() <= tol)[3:3 + at].all()
+        assert ((out.double() - want).abs() <= tol)[cu[1]:].all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_of_very_different_sizes(dim):
+    """float32: every row of a tile has a size of its own, zeros among them; and a large weight on tiny values."""
+    cu = [0, 130, 331]
+    q, k, v = fused(18, cu[-1], 4, 2, dim, torch.float32)
+    g = torch.Generator().manual_seed(1)
+    sizes = torch.exp2(torch.randint(-60, 61, (cu[-1], 1, 1), generator=g).float()).cuda()
+    check(q, k, v * sizes, cu)
+    few = torch.exp2(torch.randint(-30, 1, (cu[-1], 1, 1), generator=g).float()).cuda()
+    check(q, k * few, v, cu)
+    check(q, k * few, v * sizes, cu)
+    v2 = v * sizes
+    v2[::7] = 0
+    k2 = k * few
+    k2[::5] = 0
+    check(q, k2, v2, cu)
+    k2 = k.clone()
+    k2[0], k2[130] = 2.0, 2.0
+    q2 = q.abs() + 0.1
+    v2 = v.clone()
+    v2[0] *= 1e-6
+    v2[130] = 0
+    check(q2, k2 * 0.3, v2, cu)
+    out = woq.attn_prompt(q2, k2 * 0.3, v2 * sizes, ints(cu))
+    for _ in range(3):
+        assert torch.equal(woq.attn_prompt(q2, k2 * 0.3, v2 * sizes, ints(cu)), out)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_rows_of_very_different_sizes_that_are_not_finite(dim):
+    """float32: infinities and NaN beside finite values of all sizes."""
+    cu = [0, 301]
+    q, k, v = fused(19, 301, 4, 2, dim, torch.float32)
+    g = torch.Generator().manual_seed(2)
+    v = v * torch.exp2(torch.randint(-40, 41, (301, 1, 1), generator=g).float()).cuda()
+    want, tol = exact(q, k, v, cu, dim**-0.5)
+    for at in (0, 100, 255, 300):
+        v2 = v.clone()
+        v2[at, 0, 9], v2[at, 1, 3] = float("nan"), float("inf")
+        out = woq.attn_prompt(q, k, v2, ints(cu))
+        hit = torch.zeros(out.shape, dtype=torch.bool, device="cuda")
+        hit[at:, :2, 9] = True
+        hit[at:, 2:, 3] = True
+        assert torch.equal(~out.isfinite(), hit)
+        assert ((out.double() - want).abs() <= tol)[~hit].all()

@@ -23,8 +23,10 @@
 // inside the tensor cores, which cut off instead of rounding, run over BK keys at most; scores are one tile ahead.
 //
 // float32 rows: a kernel before writes each tile of 64 rows as two binary16 planes, high part and rest, times the
-// power of two that brings its largest finite value into [2^13, 2^14) (query rows each by itself): 22 bits of
-// every value within 2^17 of its tile's largest. Scores are three products (high x high and the two mixed
+// power of two that brings its largest finite value into [2^13, 2^14) (query rows each by itself). Where the rows' sizes
+// are not within 2^10 of one another, each row of keys or values has a power of its own, so that a row's precision
+// does not go by a larger one beside or behind it: 22 bits of every value within 2^17 of its row's largest, less what
+// the row is below the tile's largest, 2^10 at most. Scores are three products (high x high and the two mixed
 // ones, small ones first), the weights are split the same way, times 2^13. Queries turned into planes by the
 // block itself were slower (137 tokens 26 instead of 20 us, 24 prompts of 11 to 2011 715 instead of 706): one
 // block has the SM, and nothing runs under it.
@@ -33,11 +35,12 @@
 // every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory,
 // and added after the last tile to the rows that do see it.
 //
-// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20 us, 4096 234 us (24 of them the
-// planes; 1 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 698 us (124 the planes, 6.4 TB/s); 32,768
-// bfloat16 tokens 3.8 ms, 1.16 PFLOP/s, at the clock that the power cap leaves.
+// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20 us, 4096 233 us (26 of them the
+// planes; 1 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 705 us (130 the planes); 32,768
+// bfloat16 tokens 3.9 ms, 1.13 PFLOP/s.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -51,7 +54,8 @@ namespace {
 
 constexpr int kRows = 128;               // query rows of a warpgroup: the lanes of tensor memory
 constexpr int kBlockRows = 2 * kRows;
-constexpr int kSplitRows = 64;           // rows of a float32 tile with one power of two
+constexpr int kSplitRows = 64;           // rows of a float32 tile of keys or values
+constexpr int kSpread = 10;              // one power of two for them, if their sizes lie within 2^kSpread of one another
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
 constexpr uint32_t kTmemCols = 512;
@@ -73,11 +77,14 @@ struct Cfg {
   static constexpr int QBufs = MODE == kSplit ? 1 : 2;
   static constexpr int Room = 227 * 1024 - 2048 - QBufs * 2 * QBytes;
   static constexpr int Stages = Room / KvBytes > 6 ? 6 : Room / KvBytes;
-  static_assert(MODE != kSplit || BK == kSplitRows, "one power of two a tile");
+  static_assert(MODE != kSplit || BK == kSplitRows, "tiles' powers of two");
   static_assert(Stages >= 3, "keys and values of two tiles are in flight at once");
-  // Registers of a thread of the two query groups and of the helpers, out of what the block is launched with. The
-  // warps that issue matrix instructions must not spill: they set the pace.
-  static constexpr int QueryRegs = MODE == kSplit ? 216 : 200, HelperRegs = MODE == kSplit ? 72 : 104;
+  // Registers of a thread of the two query groups and of the helpers, out of what the block is launched with. float32
+  // rows of dim 128 hold an output of 128 numbers and 64 scores: 216 and 72 took 4096 tokens 250 us, 224 and 56 238,
+  // 232 and 40 233.
+  static constexpr bool Wide = MODE == kSplit && D == 128;
+  static constexpr int QueryRegs = Wide ? 232 : MODE == kSplit ? 216 : 200;
+  static constexpr int HelperRegs = Wide ? 40 : MODE == kSplit ? 72 : 104;
   static_assert(256 * QueryRegs + 128 * HelperRegs <= kThreads * kLaunchRegs, "register split");
   static constexpr int Smem = QBufs * 2 * QBytes + Stages * KvBytes + 2048;
 };
@@ -92,8 +99,8 @@ struct Args {
   int batch, q_heads, group;
   float scale;  // times log2(e)
   woq_rows o, v;
-  // float32 rows: powers of two by row (queries) and by tile of kSplitRows (keys, values)
-  const float *q_pow, *k_pow, *v_pow;
+  // float32 rows: powers of two by row (queries) and by tile of kSplitRows (keys, values); where that is negative, by row
+  const float *q_pow, *k_pow, *v_pow, *k_row, *v_row;
   int64_t tiles;  // entries of a head in k_pow and v_pow
   long long wait_limit, stuck_wait;
 };
@@ -140,6 +147,9 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
   return m;
 }
+
+// 2^e, e within +-126.
+__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 __device__ __forceinline__ void record_timeout(volatile int *abort) {
   *abort = 1;
@@ -823,86 +833,158 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(count + j + 1) & 1]);
         };
-        // A tile's weights come before the tile before it is added, whose factors are kept until then.
+        // A tile whose rows have powers of two of their own (it is rare): its scores become, in their place, the
+        // logarithms of the weights times their values' powers, less the largest, so that the tile's own code finds
+        // weights of at most 2^13. What they are to be multiplied with, the maximum and the sum are made here.
+        struct Own {
+          float m, l, alpha, v_pow;
+        };
+        auto spread_tile = [&](int j, uint32_t s_addr, float k_pow, float v_pow) {
+          const int lim = row - j * BK;
+          const int64_t first = start + static_cast<int64_t>(j) * BK;
+          const int last = static_cast<int>(min(a.tokens - 1 - first, static_cast<int64_t>(BK - 1)));
+          const float *kr = a.k_row + kv_head * a.tokens + first, *vr = a.v_row + kv_head * a.tokens + first;
+          // f(score, its column) for all columns
+          auto each = [&](auto f) {
 #pragma unroll 1
-        for (int j = 0; j < n && ok; ++j) {
+            for (int ch = 0; ch < BK; ch += 16) {
+              uint32_t x[16];
+              ptx::tmem_ld_32x32b_x16(s_addr + ch, x);
+              ptx::tmem_ld_wait(x);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(f(__uint_as_float(x[i]), ch + i));
+              ptx::tmem_st_32x32b_x16(s_addr + ch, x);
+            }
+            ptx::tmem_st_wait();
+          };
+          float top = -3.402823466e38f, high = top;  // finite, also where all scores are -infinity or NaN
+          each([&](float x, int i) {
+            x = i > lim ? -INFINITY : x * (scale * (k_pow < 0 ? __ldg(kr + min(i, last)) : k_pow));
+            top = fmaxf(top, x);
+            return x;
+          });
+          Own own;
+          own.m = fmaxf(m, top);
+          own.alpha = ex2(m - own.m);
+          own.l = l * own.alpha;
+          each([&](float x, int i) {
+            x -= own.m;
+            own.l += ex2(x + 13.0f);
+            if (i <= lim) x += ilogbf(v_pow < 0 ? __ldg(vr + min(i, last)) : v_pow);
+            high = fmaxf(high, x);
+            return x;
+          });
+          each([&](float x, int) { return x - high; });
+          own.v_pow = ex2(high);
+          return own;
+        };
+        // A tile's weights come before the tile before it is added, whose factors are kept until then.
+        auto tiles = [&](auto may_spread) {
+#pragma unroll 1
+          for (int j = 0; j < n && ok; ++j) {
+            const int64_t at = pow0 + min(static_cast<int64_t>(tile0) + j, a.tiles - 1);
+            const float k_pow = __ldg(a.k_pow + at);
+            float v_next = __ldg(a.v_pow + at);
+            const int b = (count + j) & 1;
+            if (!wait(&sh.s_full[t][b], (count + j) >> 1 & 1)) break;
+            ptx::tc_fence_after();
+            const uint32_t s_addr = tmem + lanes + t * kScores + b * BK;
+            const float alpha_last = alpha;
+            const int lim = row - j * BK;  // the last column that this row sees
+            float c = scale * k_pow;
+            Own own;
+            bool spread = false;
+            if constexpr (decltype(may_spread)::value) {
+              spread = k_pow < 0 || v_next < 0;
+              if (spread) {
+                own = spread_tile(j, s_addr, k_pow, v_next);
+                m = 0;
+                c = 1;
+              }
+            }
+            const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
+            // Four maxima and four pairs of sums, so that no addition waits for the one before.
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            float2 sum[4];
+            float2 ref;
+            const float2 cc = make_float2(c, c);
+            auto start_load = [&](int ch, uint32_t (&x)[32]) { ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x); };
+            auto mask = [&](int ch, uint32_t (&x)[32]) {
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (32 * ch + i > lim) x[i] = 0xff800000u;
+              }
+            };
+            auto top = [&](const uint32_t (&x)[32]) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
+            };
+            auto settle = [&] {
+              const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+              // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
+              const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
+              const float r = 13.0f - m2;
+              ref = make_float2(r, r);
+              alpha = ex2(m - m2);
+              l *= alpha;
+              m = m2;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sum[i] = make_float2(0, 0);
+            };
+            // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
+            auto weights = [&](int ch, const uint32_t (&x)[32]) {
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
+                y = make_float2(ex2(y.x), ex2(y.y));
+                sum[i & 3] = __fadd2_rn(sum[i & 3], y);
+                hi[i] = pack<MODE>(y.x, y.y);
+                const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
+                const float2 rest = __fadd2_rn(y, make_float2(-h.x, -h.y));
+                lo[i] = pack<MODE>(rest.x, rest.y);
+              }
+              ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
+              ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
+            };
+            uint32_t x0[32], x1[32];
+            start_load(0, x0);
+            ptx::tmem_ld_wait(x0);
+            start_load(1, x1);
+            mask(0, x0);
+            top(x0);
+            ptx::tmem_ld_wait(x1);
+            mask(1, x1);  // both are read before the weights overwrite them
+            top(x1);
+            settle();
+            weights(0, x0);
+            weights(1, x1);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) l += sum[i].x + sum[i].y;
+            if (spread) {
+              m = own.m;
+              l = own.l;
+              alpha = own.alpha;
+              v_next = own.v_pow;
+            }
+            ptx::tmem_st_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][b]);
+            if (j > 0) accumulate(j - 1, alpha_last, v_pow);
+            else if (count == 0 && lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);  // nothing to read out yet
+            v_pow = v_next;
+          }
+        };
+        // Items with such a tile have a loop of their own: a branch in the other costs it 6 %, as its registers are full.
+        bool spread = false;
+        for (int j = lane; j < n; j += 32) {
           const int64_t at = pow0 + min(static_cast<int64_t>(tile0) + j, a.tiles - 1);
-          const float k_pow = __ldg(a.k_pow + at), v_next = __ldg(a.v_pow + at);
-          const int b = (count + j) & 1;
-          if (!wait(&sh.s_full[t][b], (count + j) >> 1 & 1)) break;
-          ptx::tc_fence_after();
-          const uint32_t s_addr = tmem + lanes + t * kScores + b * BK;
-          const float alpha_last = alpha;
-          const float c = scale * k_pow;
-          const int lim = row - j * BK;  // the last column that this row sees
-          const bool masked = __any_sync(0xffffffffu, lim < BK - 1);
-          // Four maxima and four pairs of sums, so that no addition waits for the one before.
-          float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-          float2 sum[4];
-          float2 ref;
-          const float2 cc = make_float2(c, c);
-          auto start_load = [&](int ch, uint32_t (&x)[32]) { ptx::tmem_ld_32x32b_x32(s_addr + 32 * ch, x); };
-          auto mask = [&](int ch, uint32_t (&x)[32]) {
-            if (masked) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (32 * ch + i > lim) x[i] = 0xff800000u;
-            }
-          };
-          auto top = [&](const uint32_t (&x)[32]) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(x[i]));
-          };
-          auto settle = [&] {
-            const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
-            const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
-            const float r = 13.0f - m2;
-            ref = make_float2(r, r);
-            alpha = ex2(m - m2);
-            l *= alpha;
-            m = m2;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0, 0);
-          };
-          // weights 2^(s c - ref), their sum, and 16 columns of pairs (two of them when split) to write back
-          auto weights = [&](int ch, const uint32_t (&x)[32]) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float2 y = __ffma2_rn(make_float2(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), cc, ref);
-              y = make_float2(ex2(y.x), ex2(y.y));
-              sum[i & 3] = __fadd2_rn(sum[i & 3], y);
-              hi[i] = pack<MODE>(y.x, y.y);
-              const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi[i]));
-              const float2 rest = __fadd2_rn(y, make_float2(-h.x, -h.y));
-              lo[i] = pack<MODE>(rest.x, rest.y);
-            }
-            ptx::tmem_st_32x32b_x16(s_addr + 16 * ch, hi);
-            ptx::tmem_st_32x32b_x16(s_addr + BK / 2 + 16 * ch, lo);
-          };
-          uint32_t x0[32], x1[32];
-          start_load(0, x0);
-          ptx::tmem_ld_wait(x0);
-          start_load(1, x1);
-          mask(0, x0);
-          top(x0);
-          ptx::tmem_ld_wait(x1);
-          mask(1, x1);  // both are read before the weights overwrite them
-          top(x1);
-          settle();
-          weights(0, x0);
-          weights(1, x1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l += sum[i].x + sum[i].y;
-          ptx::tmem_st_wait();
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][b]);
-          if (j > 0) accumulate(j - 1, alpha_last, v_pow);
-          else if (count == 0 && lane == 0) ptx::mbar_arrive(&sh.p_full[t][0]);  // nothing to read out yet
-          v_pow = v_next;
+          spread |= fminf(__ldg(a.k_pow + at), __ldg(a.v_pow + at)) < 0;
         }
+        if (__any_sync(0xffffffffu, spread)) tiles(std::true_type());
+        else tiles(std::false_type());
         if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
         if (ok && n > 0) wait(&sh.looked_all, it & 1);
         if (ok && row < len) {
@@ -948,7 +1030,7 @@ struct SplitArgs {
   int64_t tokens, tiles;
   int batch;
   __half *planes[3][2];
-  float *q_pow, *k_pow, *v_pow;
+  float *q_pow, *k_pow, *v_pow, *k_row, *v_row;
 };
 
 constexpr int kSplitThreads = 256;
@@ -983,11 +1065,10 @@ __device__ __forceinline__ float largest_finite(float4 x) {
   auto f = [](float y) { return isfinite(y) ? fabsf(y) : 0.0f; };
   return fmaxf(fmaxf(f(x.x), f(x.y)), fmaxf(f(x.z), f(x.w)));
 }
-// The power of two that a largest value in [2^13, 2^14) takes, within 2^+-113; 2^e for such an e.
+// The power of two that a largest value in [2^13, 2^14) takes, within 2^+-113.
 __device__ __forceinline__ int exponent(float big) {
   return big > 0 ? max(min(static_cast<int>(__float_as_uint(big) >> 23) - 140, 113), -113) : 0;
 }
-__device__ __forceinline__ float power(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
 
 // Block (tile of 64 rows of a sequence, a head, or MANY of q, k and v): eight warps of eight rows, a lane four values of a
 // row.
@@ -996,7 +1077,7 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
   constexpr int LANES = D / 4, ROWS = 8 * LANES / 32;  // rows that a lane has
   __shared__ Place place;
   __shared__ int found;
-  __shared__ float warp_big[8];
+  __shared__ uint2 warp_big[8];  // the largest of a warp's rows, and the least that is not 0, less one
   ptx::pdl_wait();
   ptx::pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1020,7 +1101,6 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
     const int col = 4 * (lane % LANES);
     float4 x[ROWS];
     int row[ROWS];
-    float big = 0;
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       row[i] = place.tile * kSplitRows + warp * 8 + i * (32 / LANES) + lane / LANES;
@@ -1028,31 +1108,53 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
       if (row[i] < place.len)
         x[i] = *reinterpret_cast<const float4 *>(data + (place.start + row[i]) * src.row_stride +
                                                  head * src.head_stride + col);
-      big = larger(big, x[i]);
     }
     int ex = 0;
-    bool finite = true;
+    bool finite = true, spread = false;
+    float size = 0;  // keys, values: the largest of the row that this lane has in row_sizes()
     if (which != 0) {
-      auto of_block = [&](float b) {
+      // The block's rows: the bits of the largest value of all, and of the row with the least, if not 0, less one. Bits
+      // order what is not negative, NaN above all. The lanes of a row share the work: each step halves its rows.
+      auto row_sizes = [&](auto largest) {
+        float b[ROWS];
 #pragma unroll
-        for (int i = 1; i < 32; i <<= 1) b = larger(b, __shfl_xor_sync(0xffffffffu, b, i));
-        if (lane == 0) warp_big[warp] = b;
+        for (int i = 0; i < ROWS; ++i) b[i] = largest(x[i]);
+#pragma unroll
+        for (int n = ROWS / 2, k = LANES / 2; k > 0; n /= 2, k /= 2) {
+          const bool upper = lane & k;
+          if (n > 0) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+              const float other = __shfl_xor_sync(0xffffffffu, upper ? b[i] : b[i + n], k);
+              b[i] = larger(upper ? b[i + n] : b[i], other);
+            }
+          } else {
+            b[0] = larger(b[0], __shfl_xor_sync(0xffffffffu, b[0], k));
+          }
+        }
+        size = b[0];
+        const uint32_t bits = __float_as_uint(size);
+        const uint32_t hi = __reduce_max_sync(0xffffffffu, bits), lo = __reduce_min_sync(0xffffffffu, bits - 1);
+        if (lane == 0) warp_big[warp] = make_uint2(hi, lo);
         __syncthreads();
+        uint2 all = warp_big[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) b = larger(b, warp_big[i]);
-        return b;
+        for (int i = 1; i < 8; ++i) {
+          const uint2 w = warp_big[i];
+          all = make_uint2(max(all.x, w.x), min(all.y, w.y));
+        }
+        return all;
       };
-      big = of_block(big);
-      finite = big < INFINITY;
+      uint2 all = row_sizes([](float4 y) { return larger(0.0f, y); });
+      finite = all.x < 0x7f800000u;
       if (!finite) {
         __syncthreads();
-        big = 0;
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) big = fmaxf(big, largest_finite(x[i]));
-        big = of_block(big);
+        all = row_sizes([](float4 y) { return largest_finite(y); });
       }
-      ex = exponent(big);
-      if (threadIdx.x == 0) (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = power(ex);
+      ex = exponent(__uint_as_float(all.x));
+      spread = all.x > 0 && (all.x >> 23) - (all.y + 1 >> 23) > kSpread;
+      if (threadIdx.x == 0)
+        (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = spread ? -1.0f : power(ex);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -1067,10 +1169,16 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
           for (int k = 1; k < LANES; k <<= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, k));
         }
         ex = exponent(b);
+      } else if (spread) {
+        // row i of a lane's ROWS is with the lanes whose bits below the row's are i's, the highest first
+        constexpr int kLow = LANES / ROWS;
+        const float b = __shfl_sync(0xffffffffu, size, (lane / LANES) * LANES + i * kLow);
+        ex = b > 0 ? exponent(b) : -113;  // a row of zeros has no part in what the others are taken times
       }
       if (row[i] >= place.len) continue;
       const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
       if (which == 0 && col == 0) a.q_pow[t] = power(ex);
+      if (spread && col == 0) (which == 1 ? a.k_row : a.v_row)[t] = power(ex);
       uint2 hi, lo;
       split4(x[i], power(-ex), finite, hi, lo);
       *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
@@ -1140,9 +1248,9 @@ int launch_split(const SplitArgs &a, cudaStream_t s, const DevInfo &dev) {
   return WOQ_OK;
 }
 
-// The workspace of float32 rows: six planes, then the powers of two.
+// The workspace of float32 rows: six planes, then the powers of two, and those of single keys and values.
 struct Layout {
-  size_t plane[3], pow[3], total;
+  size_t plane[3], pow[3], row[3], total;
 };
 Layout layout(int64_t tokens, int32_t batch, int32_t hq, int32_t hk, int32_t dim) {
   Layout L;
@@ -1157,6 +1265,8 @@ Layout layout(int64_t tokens, int32_t batch, int32_t hq, int32_t hk, int32_t dim
   for (int i = 0; i < 3; ++i) {
     L.pow[i] = at;
     at += up256(heads[i] * (i == 0 ? t : tiles) * 4);
+    L.row[i] = at;
+    if (i > 0) at += up256(heads[i] * t * 4);
   }
   L.total = at;
   return L;
@@ -1215,11 +1325,16 @@ int launch_attn_prompt(const woq_rows &q, const woq_rows &k, const woq_rows &v, 
     }
   }
   if (mode == kSplit) {
-    float *pow[3];
-    for (int i = 0; i < 3; ++i) pow[i] = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.pow[i]);
+    float *pow[3], *row[3];
+    for (int i = 0; i < 3; ++i) {
+      pow[i] = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.pow[i]);
+      row[i] = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + L.row[i]);
+    }
     a.q_pow = sp.q_pow = pow[0];
     a.k_pow = sp.k_pow = pow[1];
     a.v_pow = sp.v_pow = pow[2];
+    a.k_row = sp.k_row = row[1];
+    a.v_row = sp.v_row = row[2];
     sp.q = q;
     sp.k = k;
     sp.v = v;
