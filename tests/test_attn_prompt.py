@@ -302,7 +302,7 @@ def test_thousands_of_empty_sequences(dtype):
     assert woq.device_status() == _lib.WOQ_OK
 
 
-@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("size", [2.0**20, 2.0**25, 2.0**27, 2.0**30, -(2.0**25), -(2.0**28), -(2.0**30)])
 def test_scores_far_from_zero(dtype, size):
     """Scores that are exact whole numbers times `size`: equal ones share the weight, others have none of it."""

@@ -56,6 +56,10 @@ constexpr int kRows = 128;               // query rows of a warpgroup: the lanes
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kSplitRows = 64;           // rows of a float32 tile of keys or values
 constexpr int kSpread = 10;              // one power of two for them, if their sizes lie within 2^kSpread of one another
+// A score's factor from which on float32 rows' scores may reach 2^23: they are sums of 128 products below 2^28. Above
+// that, `largest less itself` in one fused step would be what its product was rounded by, and from 2^26 on a weight of
+// that leaves binary16.
+constexpr float kFar = 0x1p-12f;
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
 constexpr uint32_t kTmemCols = 512;
@@ -833,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(count + j + 1) & 1]);
         };
-        // A tile whose rows have powers of two of their own (it is rare): its scores become, in their place, the
+        // A tile whose rows have powers of two of their own, or whose scores may be far from zero (it is rare): its scores become, in their place, the
         // logarithms of the weights times their values' powers, less the largest, so that the tile's own code finds
         // weights of at most 2^13. What they are to be multiplied with, the maximum and the sum are made here.
         struct Own {
@@ -895,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Own own;
             bool spread = false;
             if constexpr (decltype(may_spread)::value) {
-              spread = k_pow < 0 || v_next < 0;
+              spread = __any_sync(0xffffffffu, k_pow < 0 || v_next < 0 || c > kFar);
               if (spread) {
                 own = spread_tile(j, s_addr, k_pow, v_next);
                 m = 0;
@@ -978,12 +982,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         };
         // Items with such a tile have a loop of their own: a branch in the other costs it 6 %, as its registers are full.
-        bool spread = false;
+        float largest = 0, least = 1;
         for (int j = lane; j < n; j += 32) {
           const int64_t at = pow0 + min(static_cast<int64_t>(tile0) + j, a.tiles - 1);
-          spread |= fminf(__ldg(a.k_pow + at), __ldg(a.v_pow + at)) < 0;
+          const float k_pow = __ldg(a.k_pow + at);
+          largest = fmaxf(largest, k_pow);
+          least = fminf(least, fminf(k_pow, __ldg(a.v_pow + at)));
         }
-        if (__any_sync(0xffffffffu, spread)) tiles(std::true_type());
+        largest = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(largest)));
+        if (__any_sync(0xffffffffu, least < 0 || scale * largest > kFar)) tiles(std::true_type());
         else tiles(std::false_type());
         if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
         if (ok && n > 0) wait(&sh.looked_all, it & 1);
