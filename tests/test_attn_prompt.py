@@ -400,3 +400,18 @@ def test_rows_of_very_different_sizes_that_are_not_finite(dim):
         hit[at:, 2:, 3] = True
         assert torch.equal(~out.isfinite(), hit)
         assert ((out.double() - want).abs() <= tol)[~hit].all()
+
+
+def test_values_next_to_the_end_of_the_range():
+    """Finite values of up to 1e37: their weighted means are finite, and so are the sums on the way."""
+    for dim in (64, 128):
+        q, k, v = fused(20, 40, 2, 1, dim, torch.float32)
+        check(q, k, v.clamp(-3, 3) * 3e36, [0, 7, 8, 19, 40])  # a sum of 21 of them fits 32 bits
+        # a key in a later tile takes over, just less than 2^8 above the others before it. A sum of weights of at most 1 is
+        # 200e36 at most, which 32 bits hold; with the key's weight as 233 instead of 1 it would be 383e36
+        for dtype in (torch.float32, torch.bfloat16):
+            q = torch.ones(200, 1, dim, dtype=dtype, device="cuda")
+            k = torch.zeros(200, 1, dim, dtype=dtype, device="cuda")
+            k[150] = 5.45 / dim**0.5
+            v = torch.full((200, 1, dim), 1e36, dtype=dtype, device="cuda")
+            check(q, k, v, [0, 200])

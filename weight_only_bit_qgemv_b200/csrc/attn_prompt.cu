@@ -55,6 +55,8 @@ namespace {
 constexpr int kRows = 128;               // query rows of a warpgroup: the lanes of tensor memory
 constexpr int kBlockRows = 2 * kRows;
 constexpr int kSplitRows = 64;           // rows of a float32 tile of keys or values
+constexpr float kLag = 8;                // what 16-bit rows' weights may exceed 1 by, as a power of two
+constexpr int kWeightBits = 13;          // float32 rows' weights reach 2^kWeightBits
 constexpr int kSpread = 10;              // one power of two for them, if their sizes lie within 2^kSpread of one another
 // A score's factor from which on float32 rows' scores may reach 2^23: they are sums of 128 products below 2^28. Above
 // that, `largest less itself` in one fused step would be what its product was rounded by, and from 2^26 on a weight of
@@ -696,8 +698,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if constexpr (MODE != kSplit) {
         // 16-bit rows: a tile's scores in registers, the output summed in tensor memory. The weights
         // are taken against `ref`, a maximum that may lag behind: only when a row's maximum has grown by more
-        // than 2^8 is the row's output scaled down (by its own thread), which a few tiles at a row's
-        // start need. The largest weight is then 2^8, which both types hold. The maximum is taken off the scores before
+        // than 2^kLag is the row's output scaled down (by its own thread), which a few tiles at a row's
+        // start need. The largest weight is then 2^kLag; bfloat16 ones, which have the range below, are taken times
+        // 2^-kLag, so that values next to the type's end do not leave 32 bits on the way. The maximum is taken off the scores before
         // they are scaled, so that it less itself is 0 whatever its size: in one fused step it would be what its product
         // was rounded by, which is beyond binary16 for scores of 2^27 (one instruction a pair of scores less, 1.3 %).
         float ref = 0, l = 0;
@@ -741,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (j == 0) {
             ref = m;
-          } else if (__any_sync(0xffffffffu, (m - ref) * c > 8.0f)) {
+          } else if (__any_sync(0xffffffffu, (m - ref) * c > kLag)) {
             const float next = fmaxf(ref, m), alpha = ex2((ref - next) * c);
             const float2 al = make_float2(alpha, alpha);
             ref = next;
@@ -770,8 +773,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              float2 y = __fmul2_rn(
-                  __fadd2_rn(make_float2(__uint_as_float(x[ch][2 * i]), __uint_as_float(x[ch][2 * i + 1])), rr), cc);
+              float2 y =
+                  __fadd2_rn(make_float2(__uint_as_float(x[ch][2 * i]), __uint_as_float(x[ch][2 * i + 1])), rr);
+              if constexpr (MODE == kBf16) y = __ffma2_rn(y, cc, make_float2(-kLag, -kLag));
+              else y = __fmul2_rn(y, cc);
               y = make_float2(ex2(y.x), ex2(y.y));
               sum[i & 1] = __fadd2_rn(sum[i & 1], y);
               w[i] = pack<MODE>(y.x, y.y);
@@ -873,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           own.l = l * own.alpha;
           each([&](float x, int i) {
             x -= own.m;
-            own.l += ex2(x + 13.0f);
+            own.l += ex2(x + kWeightBits);
             if (i <= lim) x += ilogbf(v_pow < 0 ? __ldg(vr + min(i, last)) : v_pow);
             high = fmaxf(high, x);
             return x;
@@ -928,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float all = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
               // A finite maximum, also where all scores are -infinity or NaN: those rows end as 0 / 0.
               const float m2 = fmaxf(m, fmaxf(all * c, -3.402823466e38f));
-              const float r = 13.0f - m2;
+              const float r = kWeightBits - m2;
               ref = make_float2(r, r);
               alpha = ex2(m - m2);
               l *= alpha;
@@ -995,7 +1000,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && n > 0) accumulate(n - 1, alpha, v_pow);
         if (ok && n > 0) wait(&sh.looked_all, it & 1);
         if (ok && row < len) {
-          const float inv = 1.0f / l;
+          const float inv = static_cast<float>(1 << kWeightBits) / l;
 #pragma unroll
           for (int i = 0; i < D / 2; ++i) o[i] = make_float2(o[i].x * inv, o[i].y * inv);
 #pragma unroll
@@ -1118,6 +1123,7 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
     }
     int ex = 0;
     bool finite = true, spread = false;
+    const int less = which == 2 ? kWeightBits : 0;  // the weights' power is taken off the values'
     float size = 0;  // keys, values: the largest of the row that this lane has in row_sizes()
     if (which != 0) {
       // The block's rows: the bits of the largest value of all, and of the row with the least, if not 0, less one. Bits
@@ -1161,7 +1167,7 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
       ex = exponent(__uint_as_float(all.x));
       spread = all.x > 0 && (all.x >> 23) - (all.y + 1 >> 23) > kSpread;
       if (threadIdx.x == 0)
-        (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = spread ? -1.0f : power(ex);
+        (which == 1 ? a.k_pow : a.v_pow)[head * a.tiles + blockIdx.x] = spread ? -1.0f : power(ex - less);
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
@@ -1185,7 +1191,7 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
       if (row[i] >= place.len) continue;
       const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
       if (which == 0 && col == 0) a.q_pow[t] = power(ex);
-      if (spread && col == 0) (which == 1 ? a.k_row : a.v_row)[t] = power(ex);
+      if (spread && col == 0) (which == 1 ? a.k_row : a.v_row)[t] = power(ex - less);
       uint2 hi, lo;
       split4(x[i], power(-ex), finite, hi, lo);
       *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
