@@ -415,8 +415,9 @@ int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, in
  * largest of its token and head, the others to 2^-28 of that largest, whatever other tokens' sizes are; weights
  * likewise, 22 bits within 2^16 of the row's largest and the others to 2^-38 of it; three products on the tcgen05
  * tensor cores, FP32 sums. 16-bit: operands as they are, weights rounded to the type. The lengths stay on the device; the grid
- * goes by tokens and batch. Deterministic. A value that is not finite enters only rows that see it: a
- * row that sees such a q or k is NaN, one that sees such a v is not finite in its column.
+ * goes by tokens and batch. Deterministic. A value that is not finite enters only rows that see it:
+ * one that sees such a v is not finite in its column; one that sees such a q or k is NaN (float32), or what its
+ * scores make it (16-bit: one of -infinity weighs nothing, one of +infinity or NaN makes the row NaN).
  * batch 1 to 65536; (tokens / 256 + batch) * q.heads < 2^31; tokens == 0 does nothing.
  * Errors: WOQ_EINVAL (null pointers, dtypes, heads, batch, scale, overlap), WOQ_ESHAPE (dim, sizes, strides),
  * WOQ_EALIGN, WOQ_EWORKSPACE, WOQ_EDEVICE, WOQ_ECUDA. Waits inside the kernel are bounded, as qgemm's.

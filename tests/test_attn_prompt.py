@@ -415,3 +415,38 @@ def test_values_next_to_the_end_of_the_range():
             k[150] = 5.45 / dim**0.5
             v = torch.full((200, 1, dim), 1e36, dtype=dtype, device="cuda")
             check(q, k, v, [0, 200])
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("value", [float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 100, 200, 300])
+def test_infinite_keys_and_queries(dtype, value, at):
+    """float32: a row that sees an infinity in a key, or has one, is NaN. 16-bit rows go by the scores: one of -infinity
+    weighs nothing, one of +infinity and NaN make the row NaN."""
+    cu = [0, 301, 420]
+    q, k, v = fused(21, 420, 4, 2, 64, dtype)
+    clean, bound = exact(q, k, v, cu, 0.125)
+    q2, k2 = q.clone(), k.clone()
+    k2[at, 0, 1] = value
+    out = woq.attn_prompt(q, k2, v, ints(cu))
+    hit = torch.zeros(420, 4, 64, dtype=torch.bool, device="cuda")
+    hit[at:301, :2] = True
+    if dtype == torch.float32:
+        assert torch.equal(out.isnan(), hit)
+    else:
+        want, tol = exact(q, k2, v, cu, 0.125)
+        assert want.isnan().any() and torch.equal(out.isnan(), want.isnan())
+        assert at == 300 or want[at + 1:301, :2].isfinite().any()  # the last row has no others behind it
+        seen = want.isfinite() & tol.isfinite()  # rows that see it have an infinite bound
+        assert ((out.double() - want).abs() <= tol)[seen].all()
+        # of those, exact()'s terms with what bounds them: half a step of weight and result, three in all, of at most max |v|,
+        # and of the finite scores, whose sum |q k| scale is below 64 here, 2^-16 of that: two half steps of binary16
+        want = want[at:301, :2]
+        assert ((out[at:301, :2].double() - want).abs() <= 8 * ref.UNIT[dtype] * v.abs().max())[want.isfinite()].all()
+    # The other rows are as exact as without it. They need not have the same bits: rows of a warp are scaled down together.
+    assert ((out.double() - clean).abs() <= bound)[~hit].all()
+    q2[at, 1, 5] = value
+    out = woq.attn_prompt(q2, k, v, ints(cu))
+    hit[:] = False
+    hit[at, 1] = True
+    assert torch.equal(out.isnan(), hit) and ((out.double() - clean).abs() <= bound)[~hit].all()

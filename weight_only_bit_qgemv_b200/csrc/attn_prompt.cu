@@ -1192,6 +1192,15 @@ __global__ void __launch_bounds__(kSplitThreads, 4) attn_split_kernel(const Spli
       const int64_t t = static_cast<int64_t>(head) * a.tokens + place.start + row[i];
       if (which == 0 && col == 0) a.q_pow[t] = power(ex);
       if (spread && col == 0) (which == 1 ? a.k_row : a.v_row)[t] = power(ex - less);
+      if (!finite && which != 2) {
+        // An infinity in a query or key becomes NaN: beside the low plane's zeros and signs its products would be infinite
+        // or NaN by chance.
+        auto nan = [](float &y) { y = isfinite(y) ? y : __int_as_float(0x7fffffff); };
+        nan(x[i].x);
+        nan(x[i].y);
+        nan(x[i].z);
+        nan(x[i].w);
+      }
       uint2 hi, lo;
       split4(x[i], power(-ex), finite, hi, lo);
       *reinterpret_cast<uint2 *>(a.planes[which][0] + t * D + col) = hi;
