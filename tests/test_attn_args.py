@@ -185,3 +185,29 @@ def test_no_rows_and_interleaved_arrays():
         (rows(row=768, head=256), rows(data=OK + 64 * 4, row=768, head=256)),  # half a row
     ):
         assert gather(a, b) == gather(b, a) == _lib.WOQ_EINVAL
+
+
+def test_strides_and_extents_that_nothing_can_hold():
+    """Strides of 2^40 bytes, arrays beyond 64 bits of offsets, more rows than a grid has blocks for."""
+    L = _lib.lib()
+
+    def gather(a, b, tokens=4, c=None):
+        return L.kv4_gather(ctypes.byref(c or kv4()), OK, None, 1, OK, 1, tokens, ctypes.byref(a), ctypes.byref(b), None)
+
+    def prompt(q, tokens=4):
+        k, o = rows(heads=1, data=3 * FAR, dtype=q.dtype), rows(heads=1, data=5 * FAR, dtype=q.dtype)
+        return L.attn_prompt(ctypes.byref(q), ctypes.byref(k), ctypes.byref(k), tokens, OK, 1, 128, 0.1, ctypes.byref(o),
+                             1 << 21, 1 << 62, None)
+
+    for dtype, size in ((0, 4), (1, 2), (2, 2)):
+        for stride in (2**40 // size, 2**40 - 16, 2**62):
+            assert gather(rows(dtype=dtype, row=stride), rows(data=FAR, dtype=dtype)) == _lib.WOQ_ESHAPE
+            assert gather(rows(dtype=dtype, head=stride, row=128), rows(data=FAR, dtype=dtype)) == _lib.WOQ_ESHAPE
+            assert prompt(rows(heads=1, dtype=dtype, row=stride)) == _lib.WOQ_ESHAPE
+        wide = 2**40 // size - 64
+        assert gather(rows(dtype=dtype, row=wide), rows(data=FAR, dtype=dtype), tokens=2**30) == _lib.WOQ_ESHAPE
+        assert prompt(rows(heads=1, dtype=dtype, row=wide), tokens=2**30) == _lib.WOQ_ESHAPE
+        # appended rows may share elements, so that this many are no more than 32 GB
+        k, c = rows(dtype=dtype, heads=1024, row=16 // size, head=128), kv4(heads=1024)
+        assert L.kv4_append(ctypes.byref(c), ctypes.byref(k), ctypes.byref(k), 2**31 - 1, OK, None, 1, OK, 1,
+                            None) == _lib.WOQ_ESHAPE

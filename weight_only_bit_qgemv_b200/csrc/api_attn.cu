@@ -21,11 +21,13 @@ int check_rows(const woq_rows *r, int64_t rows, int64_t heads, int64_t dim) {
   if (!r || (rows > 0 && !r->data)) return WOQ_EINVAL;
   if (r->dtype != WOQ_F32 && r->dtype != WOQ_F16 && r->dtype != WOQ_BF16) return WOQ_EINVAL;
   if (r->heads != heads) return WOQ_EINVAL;
-  const int64_t unit = 16 / size_of(r->dtype);
-  // strides below 2^40 elements: offsets stay far from the end of 64 bits for any count of rows
-  if (r->row_stride <= 0 || r->head_stride < dim || r->row_stride >= (int64_t(1) << 40) ||
-      r->head_stride >= (int64_t(1) << 40) || r->row_stride % unit || r->head_stride % unit)
+  const int64_t size = size_of(r->dtype), unit = 16 / size, most = (int64_t(1) << 40) / size;
+  // strides below 2^40 bytes, which a tensor map holds, and an array within 2^62: its offsets fit 64 bits
+  if (r->row_stride <= 0 || r->head_stride < dim || r->row_stride >= most || r->head_stride >= most ||
+      r->row_stride % unit || r->head_stride % unit)
     return WOQ_ESHAPE;
+  const __int128 bytes = (static_cast<__int128>(rows - 1) * r->row_stride + (heads - 1) * r->head_stride + dim) * size;
+  if (rows > 0 && bytes > (__int128(1) << 62)) return WOQ_ESHAPE;
   return aligned(r->data, 16) ? WOQ_OK : WOQ_EALIGN;
 }
 
@@ -86,7 +88,11 @@ int check_step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64
   if (tokens > INT32_MAX) return WOQ_ESHAPE;
   if (!aligned(cu, 4) || !aligned(start, 4)) return WOQ_EALIGN;
   rc = check_rows(k, tokens, cache->kv_heads, cache->dim);
-  return rc != WOQ_OK ? rc : check_rows(v, tokens, cache->kv_heads, cache->dim);
+  if (rc != WOQ_OK) return rc;
+  rc = check_rows(v, tokens, cache->kv_heads, cache->dim);
+  if (rc != WOQ_OK) return rc;
+  // pairs of heads, 32 of them a block at most
+  return tokens * ((cache->kv_heads + 1) / 2) > (int64_t(INT32_MAX) << 5) ? WOQ_ESHAPE : WOQ_OK;
 }
 
 int step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
