@@ -340,7 +340,8 @@ int qgemm_bf16_noalloc(const float *X, int64_t m, const woq_weight *w, float *Y,
  * Rows of heads in device memory: element (t, h, d) is at data + t * row_stride +
  * h * head_stride + d, strides in elements. A slice of a fused projection's output [t, q | k | v]
  * is such an array. data is 16-byte aligned (NULL for no rows) and both strides are positive multiples
- * of 16 bytes below 2^40 bytes; head_stride is at least the heads' dim.
+ * of 16 bytes below 2^40 bytes; head_stride is at least the heads' dim. No two rows of heads of an array
+ * that is written share an element.
  */
 typedef struct woq_rows {
   void *data;

@@ -211,3 +211,40 @@ def test_strides_and_extents_that_nothing_can_hold():
         k, c = rows(dtype=dtype, heads=1024, row=16 // size, head=128), kv4(heads=1024)
         assert L.kv4_append(ctypes.byref(c), ctypes.byref(k), ctypes.byref(k), 2**31 - 1, OK, None, 1, OK, 1,
                             None) == _lib.WOQ_ESHAPE
+
+
+def test_written_arrays_whose_rows_share_elements():
+    L = _lib.lib()
+    through = (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE)
+    big = {"data": 16 * FAR}
+
+    def attn(o, batch=3):
+        q, c = rows(heads=o.heads, row=128 * o.heads), kv4(heads=1)
+        return L.kv4_attn(ctypes.byref(q), ctypes.byref(c), OK, batch, OK, 1, 0.1, ctypes.byref(o), 1 << 21, 1 << 30, None)
+
+    def prompt(o, tokens=3):
+        q, k = rows(heads=o.heads, row=128 * o.heads), rows(heads=1, data=3 * FAR)
+        return L.attn_prompt(ctypes.byref(q), ctypes.byref(k), ctypes.byref(k), tokens, OK, 1, 128, 0.1, ctypes.byref(o),
+                             1 << 21, 1 << 30, None)
+
+    def gather(o, tokens=3):
+        v, c = rows(data=5 * FAR, heads=o.heads, row=128 * o.heads), kv4(heads=o.heads)
+        return L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, tokens, ctypes.byref(o), ctypes.byref(v), None)
+
+    def gather_v(o, tokens=3):
+        k, c = rows(data=5 * FAR, heads=o.heads, row=128 * o.heads), kv4(heads=o.heads)
+        return L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, tokens, ctypes.byref(k), ctypes.byref(o), None)
+
+    for o in (rows(heads=1, row=16, **big), rows(heads=1, row=124, **big), rows(heads=2, row=128, head=128, **big),
+              rows(heads=2, row=128, head=256, **big), rows(heads=2, row=192, head=128, **big),
+              rows(heads=3, row=256, head=320, **big), rows(heads=4, row=400, head=132, **big)):
+        for call in (attn, prompt, gather, gather_v):
+            assert call(o) == _lib.WOQ_ESHAPE, (o.heads, o.row_stride, o.head_stride)
+    if not torch.cuda.is_available():  # these would run
+        for o in (rows(heads=1, row=128, **big), rows(heads=2, row=256, head=128, **big),
+                  rows(heads=2, row=128, head=384, **big), rows(heads=2, row=132, head=392, **big),
+                  rows(heads=2, row=256, head=640, **big), rows(heads=3, row=384, head=512, **big)):
+            for call in (attn, prompt, gather, gather_v):
+                assert call(o) in through, (o.heads, o.row_stride, o.head_stride)
+        for o in (rows(heads=1, row=16, **big), rows(heads=2, row=16, head=128, **big)):  # a single row
+            assert attn(o, 1) in through and prompt(o, 1) in through and gather(o, 1) in through

@@ -45,6 +45,19 @@ int check_table(int32_t batch, const int32_t *table, int64_t width) {
   return aligned(table, 4) ? WOQ_OK : WOQ_EALIGN;
 }
 
+// An array that is written (it passed check_rows): no two rows of heads share an element.
+int check_written(const woq_rows *r, int64_t rows, int64_t dim) {
+  const int64_t row = r->row_stride, head = r->head_stride, heads = r->heads;
+  if (rows <= 1) return WOQ_OK;
+  if (row < dim) return WOQ_ESHAPE;
+  if (row >= (heads - 1) * head + dim || head >= (rows - 1) * row + dim) return WOQ_OK;  // one within the other
+  for (int64_t h = 1; h < heads; ++h) {  // the two rows that lie next to h heads on
+    const int64_t i = h * head / row, before = h * head - i * row;
+    if ((i < rows && before < dim) || (i + 1 < rows && row - before < dim)) return WOQ_ESHAPE;
+  }
+  return WOQ_OK;
+}
+
 // First and one past the last byte of [rows, heads, dim].
 struct Span {
   uintptr_t first, last;
@@ -99,7 +112,14 @@ int step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tok
          const int32_t *start, int32_t batch, const int32_t *table, int64_t width, bool append, void *stream) {
   int rc = check_step(cache, k, v, tokens, cu, start, batch, table, width);
   if (rc != WOQ_OK) return rc;
-  if (!append && tokens > 0 && overlap(*k, *v, tokens, cache->dim)) return WOQ_EINVAL;
+  if (!append && tokens > 0) {
+    rc = check_written(k, tokens, cache->dim);
+    if (rc != WOQ_OK) return rc;
+    rc = check_written(v, tokens, cache->dim);
+    if (rc != WOQ_OK) return rc;
+    if (overlap(*k, *v, tokens, cache->dim))
+      return WOQ_EINVAL;
+  }
   DevInfo dev;
   rc = current_device(&dev);
   if (rc != WOQ_OK || tokens == 0) return rc;
@@ -145,6 +165,8 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
   if (rc != WOQ_OK) return rc;
   rc = woq::check_rows(o, batch, q->heads, cache->dim);
   if (rc != WOQ_OK) return rc;
+  rc = woq::check_written(o, batch, cache->dim);
+  if (rc != WOQ_OK) return rc;
   if (o->dtype != q->dtype || !(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
   if (!woq::aligned(lens, 4)) return WOQ_EALIGN;
   if (woq::overlap(*q, *o, batch, cache->dim)) return WOQ_EINVAL;
@@ -185,6 +207,8 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
   if (!(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
   if (!woq::aligned(cu, 4)) return WOQ_EALIGN;
   if (tokens > INT32_MAX || (tokens / 256 + batch) * q->heads > INT32_MAX) return WOQ_ESHAPE;
+  const int rc_o = woq::check_written(o, tokens, dim);
+  if (rc_o != WOQ_OK) return rc_o;
   if (tokens > 0)
     for (int i = 0; i < 3; ++i)
       if (woq::overlap(*all[i], *o, tokens, dim)) return WOQ_EINVAL;
