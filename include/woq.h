@@ -395,7 +395,7 @@ int kv4_append(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64
  * kv4_gather -- reads rows of the cache back, scale * code, addressed as kv4_append addresses them
  * (a float32 result is exact; 16-bit ones are rounded once). A row of a sequence whose token has no
  * page becomes 0; rows outside the sequences are left as they are. Arguments and errors as
- * kv4_append, with k and v written, and WOQ_EINVAL where they share bytes.
+ * kv4_append, with k and v written, and WOQ_EINVAL where they share bytes with one another or the cache.
  */
 int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, int32_t batch, const int32_t *table,
                int64_t width, int64_t tokens, const woq_rows *k, const woq_rows *v, void *stream);
@@ -442,7 +442,7 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
  *   table   device, int32 [batch, width]; tokens in a page outside [0, pages) are not there, and
  *           a sequence with no other tokens gives a zero row
  *   scale   positive and finite, usually dim^-1/2
- *   o       device, as q, of q's type, not overlapping q; fully written
+ *   o       device, as q, of q's type, not overlapping q or the cache; fully written
  *   workspace  device, 256-byte aligned, at least kv4_attn_workspace_bytes. It must be zero before
  *           the first call, and every call leaves its counters zero (after a WOQ_ETIMEOUT from
  *           woq_device_status, zero it before reuse); its size goes by batch and heads, not by
@@ -451,7 +451,7 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
  * batch 1 to 4096. One launch whose grid does not depend on the lengths. Non-finite values in q, or in a
  * block of a token that is attended to, make the results they enter NaN; nothing else of the
  * cache's pages, such as slots behind the last token, has an influence.
- * Errors: as kv4_append, WOQ_EINVAL for scale and an o that overlaps q, WOQ_EWORKSPACE.
+ * Errors: as kv4_append, WOQ_EINVAL for scale and an o that overlaps q or the cache, WOQ_EWORKSPACE.
  */
 size_t kv4_attn_workspace_bytes(const woq_kv4 *cache, int32_t q_heads, int32_t batch);
 int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32_t batch, const int32_t *table,

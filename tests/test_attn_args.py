@@ -248,3 +248,22 @@ def test_written_arrays_whose_rows_share_elements():
                 assert call(o) in through, (o.heads, o.row_stride, o.head_stride)
         for o in (rows(heads=1, row=16, **big), rows(heads=2, row=16, head=128, **big)):  # a single row
             assert attn(o, 1) in through and prompt(o, 1) in through and gather(o, 1) in through
+
+
+def test_results_on_the_cache():
+    L = _lib.lib()
+    c = kv4()  # 4 pages of 16 tokens, 2 heads: 16384 bytes of codes, 2048 of scales
+    far = rows(data=8 * FAR)
+    for at, on in ((FAR - 4 * 1024, False), (FAR - 4 * 1024 + 16, True), (FAR + 16384 - 16, True), (FAR + 16384, False),
+                   (2 * FAR, True), (2 * FAR + 2048, False), (2 * FAR - 4 * 1024, False)):
+        r = rows(data=at)  # 4 rows of 2 heads of 128 float32
+        q = rows(heads=2, data=9 * FAR)
+        calls = [lambda: L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, 4, ctypes.byref(r), ctypes.byref(far), None),
+                 lambda: L.kv4_gather(ctypes.byref(c), OK, None, 1, OK, 1, 4, ctypes.byref(far), ctypes.byref(r), None),
+                 lambda: L.kv4_attn(ctypes.byref(q), ctypes.byref(c), OK, 4, OK, 1, 0.1, ctypes.byref(r), 1 << 21, 1 << 30,
+                                    None)]
+        for call in calls:
+            if on:
+                assert call() == _lib.WOQ_EINVAL
+            elif not torch.cuda.is_available():  # it would run
+                assert call() in (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE)

@@ -91,6 +91,17 @@ bool overlap(const woq_rows &a, const woq_rows &b, int64_t rows, int64_t dim) {
   return true;
 }
 
+// Whether an array shares bytes with the cache.
+bool on_cache(const woq_rows &r, int64_t rows, const woq_kv4 &c) {
+  const Span x = span(r, rows, c.dim);
+  const __int128 tokens = static_cast<__int128>(c.pages) * c.kv_heads * c.page;
+  auto on = [&](const void *p, __int128 bytes) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(p);
+    return x.first < first + bytes && first < x.last;
+  };
+  return on(c.codes, tokens * c.dim) || on(c.scales, tokens * (c.dim / 8));
+}
+
 int check_step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tokens, const int32_t *cu,
                const int32_t *start, int32_t batch, const int32_t *table, int64_t width) {
   int rc = check_cache(cache);
@@ -117,7 +128,7 @@ int step(const woq_kv4 *cache, const woq_rows *k, const woq_rows *v, int64_t tok
     if (rc != WOQ_OK) return rc;
     rc = check_written(v, tokens, cache->dim);
     if (rc != WOQ_OK) return rc;
-    if (overlap(*k, *v, tokens, cache->dim))
+    if (overlap(*k, *v, tokens, cache->dim) || on_cache(*k, tokens, *cache) || on_cache(*v, tokens, *cache))
       return WOQ_EINVAL;
   }
   DevInfo dev;
@@ -176,6 +187,7 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
                                               rc == WOQ_OK ? dev.sm_count : 148);
   if (!workspace || workspace_bytes < need) return WOQ_EWORKSPACE;
   if (!woq::aligned(workspace, 256)) return WOQ_EALIGN;
+  if (woq::on_cache(*o, batch, *cache)) return WOQ_EINVAL;
   if (rc != WOQ_OK) return rc;
   return woq::launch_kv4_attn(*q, *cache, lens, batch, table, width, scale, *o, workspace,
                               static_cast<cudaStream_t>(stream), dev);
