@@ -409,7 +409,7 @@ int kv4_gather(const woq_kv4 *cache, const int32_t *cu, const int32_t *start, in
  *           overlaps none of the others. Slices of one fused projection are fine.
  *   cu      device, int32 [batch + 1], non-decreasing; sequences may be empty. Rows before cu[0] and
  *           from cu[batch] on are not written, and have no influence
- *   scale   positive and finite, usually dim^-1/2
+ *   scale   positive, at most 2^127, usually dim^-1/2
  *   workspace  device, 256-byte aligned, attn_prompt_workspace_bytes(...) bytes (0 for 16-bit types);
  *           its contents on entry do not matter; calls that share one must be ordered on one stream
  * float32: q, k and v as two binary16 planes each: 22 significant bits of every value within 2^7 of the
@@ -441,7 +441,7 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
  *           0 or less gives a zero row; more than width * page counts as that
  *   table   device, int32 [batch, width]; tokens in a page outside [0, pages) are not there, and
  *           a sequence with no other tokens gives a zero row
- *   scale   positive and finite, usually dim^-1/2
+ *   scale   positive, at most 2^127, usually dim^-1/2
  *   o       device, as q, of q's type, not overlapping q or the cache; fully written
  *   workspace  device, 256-byte aligned, at least kv4_attn_workspace_bytes. It must be zero before
  *           the first call, and every call leaves its counters zero (after a WOQ_ETIMEOUT from

@@ -267,3 +267,15 @@ def test_results_on_the_cache():
                 assert call() == _lib.WOQ_EINVAL
             elif not torch.cuda.is_available():  # it would run
                 assert call() in (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE)
+
+
+def test_scales_next_to_the_end_of_the_range():
+    L = _lib.lib()
+    q, k, o, c = rows(heads=2), rows(data=3 * FAR), rows(data=4 * FAR, heads=2), kv4()
+    for scale, good in ((2.0**127, True), (1e-44, True), (1.8e38, False), (3.4e38, False)):
+        if good and torch.cuda.is_available():  # it would run
+            continue
+        got = (L.kv4_attn(ctypes.byref(q), ctypes.byref(c), OK, 2, OK, 1, scale, ctypes.byref(o), 1 << 21, 1 << 30, None),
+               L.attn_prompt(ctypes.byref(q), ctypes.byref(k), ctypes.byref(k), 4, OK, 1, 128, scale, ctypes.byref(o),
+                             1 << 21, 1 << 30, None))
+        assert all((x in (_lib.WOQ_ECUDA, _lib.WOQ_EDEVICE)) if good else x == _lib.WOQ_EINVAL for x in got)

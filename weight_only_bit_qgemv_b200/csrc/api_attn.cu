@@ -1,7 +1,6 @@
 // C-ABI entry points of the attention calls (declared in include/woq.h): argument checks, the
 // device check and dispatch to the kernel launchers. Nothing here allocates or synchronises.
 #include <algorithm>
-#include <cmath>
 #include <cstdint>
 
 #include "woq.h"
@@ -14,6 +13,9 @@ constexpr int kMaxSequences = 1 << 16;  // a tile is looked up among them in a m
 constexpr int kMaxGroup = 64;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// The kernels take it times log2(e).
+bool good_scale(float scale) { return scale > 0.0f && scale <= 0x1p127f; }
 
 int64_t size_of(int32_t dtype) { return dtype == WOQ_F32 ? 4 : 2; }
 
@@ -178,7 +180,7 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
   if (rc != WOQ_OK) return rc;
   rc = woq::check_written(o, batch, cache->dim);
   if (rc != WOQ_OK) return rc;
-  if (o->dtype != q->dtype || !(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
+  if (o->dtype != q->dtype || !woq::good_scale(scale)) return WOQ_EINVAL;
   if (!woq::aligned(lens, 4)) return WOQ_EALIGN;
   if (woq::overlap(*q, *o, batch, cache->dim)) return WOQ_EINVAL;
   DevInfo dev;
@@ -216,7 +218,7 @@ int attn_prompt(const woq_rows *q, const woq_rows *k, const woq_rows *v, int64_t
     if (rc != WOQ_OK) return rc;
     if (all[i]->dtype != q->dtype) return WOQ_EINVAL;
   }
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return WOQ_EINVAL;
+  if (!woq::good_scale(scale)) return WOQ_EINVAL;
   if (!woq::aligned(cu, 4)) return WOQ_EALIGN;
   if (tokens > INT32_MAX || (tokens / 256 + batch) * q->heads > INT32_MAX) return WOQ_ESHAPE;
   const int rc_o = woq::check_written(o, tokens, dim);
