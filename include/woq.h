@@ -467,13 +467,14 @@ int kv4_attn(const woq_rows *q, const woq_kv4 *cache, const int32_t *lens, int32
 int woq_device_status(int clear);
 
 /*
- * woq_debug_set_wait_limit -- test hook for the bounded waits of the tensor-core qgemm kernel
- * and of qgemv_chain, applied to launches that follow. cycles > 0 sets the cycle budget of
- * every wait (qgemv_chain: of its waits for weights and for the other CTAs); in qgemv_chain,
+ * woq_debug_set_wait_limit -- test hook for the bounded waits of the tensor-core qgemm kernel,
+ * qgemv_chain, attn_prompt and kv4_attn, applied to launches that follow. cycles > 0 sets the cycle
+ * budget of every wait (qgemv_chain: of its waits for weights and for the other CTAs); in qgemv_chain,
  * cycles < 0 makes each CTA's waits for the other CTAs wait for one arrival more than there
  * are CTAs, bounded by -cycles cycles, so they give up deterministically;
  * 0 restores the default (2^32 cycles, about two seconds); cycles < 0 keeps the default
- * and makes the MMA-issuing thread of every CTA first wait on a barrier that nothing
+ * and makes the MMA-issuing thread of every CTA (attn_prompt: both MMA-issuing warps; kv4_attn: every
+ * warp of a block that has tokens) first wait on a barrier that nothing
  * arrives on, bounded by -cycles cycles, so the give-up path runs deterministically
  * without a hang (the kernel then records the event, drains, frees tensor memory and
  * returns; woq_device_status reports WOQ_ETIMEOUT). Process-wide host state; not

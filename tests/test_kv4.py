@@ -499,3 +499,23 @@ def test_attention_scores_far_from_zero(size):
     v = v[:, 0].reshape(-1, 64)
     big = np.repeat(np.abs(v).reshape(-1, 2, 32).max(-1), 32, axis=-1)
     assert (np.abs(out - p @ v) <= ref.tolerance_by_column(p @ v, 0.0, p @ big, q.dtype)).all()
+
+
+def test_attention_a_wait_that_gives_up_is_reported_and_the_context_survives():
+    rng = np.random.default_rng(21)
+    cache = random_cache(rng, 64, 2, 128, 64)
+    q = torch.from_numpy(rng.standard_normal((2, 4, 128)).astype(np.float32)).cuda()
+    lens, table = ints([2048, 1500]), ints(np.arange(64).reshape(2, 32))
+    ws = woq.kv4_attn_workspace(cache, q)
+    want = woq.kv4_attn(q, cache, lens, table, workspace=ws)
+    assert woq.device_status(clear=True) == _lib.WOQ_OK
+    L = _lib.lib()
+    try:
+        L.woq_debug_set_wait_limit(-200000)
+        woq.kv4_attn(q, cache, lens, table, workspace=ws)
+        assert woq.device_status(clear=True) == _lib.WOQ_ETIMEOUT
+    finally:
+        L.woq_debug_set_wait_limit(0)
+    ws.zero_()
+    assert torch.equal(woq.kv4_attn(q, cache, lens, table, workspace=ws), want)
+    assert woq.device_status(clear=True) == _lib.WOQ_OK

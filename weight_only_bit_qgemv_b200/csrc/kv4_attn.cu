@@ -85,7 +85,7 @@ struct Args {
   float scale;
   unsigned *counters;
   float *partials;
-  long long wait_limit;
+  long long wait_limit, stuck_wait;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -157,7 +157,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   uint4 *qop = reinterpret_cast<uint4 *>(smem + kWarps * kStages * S::Stage);
   float *results = reinterpret_cast<float *>(qop + 2 * NB * 32);
   uint64_t *bars = reinterpret_cast<uint64_t *>(results + kWarps * S::Slot);
-  float *fac = reinterpret_cast<float *>(bars + kWarps * kStages);   // [kHeads]
+  uint64_t *never = bars + kWarps * kStages;                         // nothing arrives on it
+  float *fac = reinterpret_cast<float *>(never + 1);                 // [kHeads]
   int *flags = reinterpret_cast<int *>(fac + kHeads);                // abort, last, parts, sequences that have tokens
   int64_t *pre = reinterpret_cast<int64_t *>(flags + 4);             // [batch + 1]: units before a sequence
 
@@ -167,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
   const Magic magic;
 
   if (tid == 0) {
-    for (int i = 0; i < kWarps * kStages; ++i) ptx::mbar_init(&bars[i], 1);
+    for (int i = 0; i < kWarps * kStages + 1; ++i) ptx::mbar_init(&bars[i], 1);
     ptx::fence_mbar_init();
     flags[0] = 0;
     pre[0] = 0;
@@ -311,6 +312,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     for (int i = 0; i < kStages; ++i) issue(u_begin + warp + i * kWarps, i, e[i]);
   };
   if (begin < end) enter(begin);
+  if (a.stuck_wait > 0 && begin < end) {  // test hook
+    if (!ptx::mbar_wait_bounded(never, 0, a.stuck_wait, abort)) {
+      *abort = 1;
+      atomicOr(&g_kv4_timeout_flag, 1u);
+    }
+  }
 
   for (int64_t cur = begin; cur < end;) {
     const int h0 = (pass % a.chunks) * kHeads;
@@ -748,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
     cur = after;
     if (*abort) {  // uniform: read behind a barrier, written before it
       // The copies that this warp still has in flight end before the block does (or the wait for none gives up).
-      int never = 0;
-      for (int i = 0; i < kStages; ++i) ptx::mbar_wait_bounded(&bar[i], phases >> i & 1, 1LL << 28, &never);
+      int no_abort = 0;
+      for (int i = 0; i < kStages; ++i) ptx::mbar_wait_bounded(&bar[i], phases >> i & 1, 1LL << 28, &no_abort);
       break;
     }
   }
@@ -759,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 template <int D>
 size_t smem_bytes(int batch) {
   using S = Shape<D>;
-  return static_cast<size_t>(kWarps) * (kStages * S::Stage + S::Slot * 4) + 2 * S::NB * 32 * 16 + kWarps * kStages * 8 +
+  return static_cast<size_t>(kWarps) * (kStages * S::Stage + S::Slot * 4) + 2 * S::NB * 32 * 16 + (kWarps * kStages + 1) * 8 +
          (kHeads + 4) * 4 + 8 * (static_cast<size_t>(batch) + 1);
 }
 
@@ -824,6 +831,7 @@ int launch_kv4_attn(const woq_rows &q, const woq_kv4 &c, const int32_t *lens, in
   a.counters = reinterpret_cast<unsigned *>(static_cast<uint8_t *>(workspace) + partials_bytes(dev.sm_count));
   const long long lim = wait_limit_cycles();
   a.wait_limit = lim > 0 ? lim : kWaitLimit;
+  a.stuck_wait = lim < 0 ? -lim : 0;
   return c.dim == 128 ? launch<128>(a, s, dev) : launch<64>(a, s, dev);
 }
 
