@@ -450,3 +450,14 @@ def test_infinite_keys_and_queries(dtype, value, at):
     hit[:] = False
     hit[at, 1] = True
     assert torch.equal(out.isnan(), hit) and ((out.double() - clean).abs() <= bound)[~hit].all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_ends_out_of_order_leave_the_sequences_beside_them_right(dtype):
+    q, k, v = fused(22, 500, 2, 1, 64, dtype)
+    out = woq.attn_prompt(q, k, v, ints([-7, 0, 100, 300, 250, 2**31 - 1]))
+    want, tol = exact(q, k, v, [0, 100], 0.125)  # rows 250..299 are two sequences', and 300.. see them
+    assert ((out.double() - want).abs() <= tol)[:100].all()
+    want, tol = exact(q, k, v, [100, 300], 0.125)
+    assert ((out.double() - want).abs() <= tol)[100:192].all()  # whole tiles of 64 rows before the shared ones
+    assert woq.device_status() == _lib.WOQ_OK
