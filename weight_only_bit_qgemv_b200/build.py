@@ -3,6 +3,7 @@
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
 
@@ -19,6 +20,10 @@ CXX_SOURCES = ["qpack.cpp"]
 HEADERS = ["ptx.cuh", "woq_internal.h", "gemv_math.cuh", "kv4.cuh"]
 
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
+# Kernels that move registers between their warps (setmaxnreg) wait forever if the compiler gives a thread fewer at the
+# launch than their source counts on: (constant in the source, part of the kernels' names).
+LAUNCH_REGS = {"attn_prompt.cu": ("kLaunchRegs", "attn_prompt_kernel")}
+
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-I", INCLUDE, "-I", CSRC, "-Xcompiler", "-fPIC"]
 
@@ -28,6 +33,18 @@ def _stale(out: str, deps: list[str]) -> bool:
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def check_registers(src: str, source: str, log: str) -> None:
+    """Raises if ptxas gave a kernel of ``src`` other registers than its source (LAUNCH_REGS) counts on."""
+    if src not in LAUNCH_REGS:
+        return
+    constant, kernel = LAUNCH_REGS[src]
+    want = int(re.search(rf"\b{constant} = (\d+);", source).group(1))
+    used = re.findall(r"Compiling entry function '([^']*)'.*?Used (\d+) registers", log, flags=re.S)
+    got = {name: int(n) for name, n in used if kernel in name}
+    if not got or any(n != want for n in got.values()):
+        raise RuntimeError(f"{src}: {kernel} has to be launched with {want} registers a thread, the compiler gave {got}")
 
 
 def build(verbose: bool = False, force: bool = False) -> str:
@@ -56,6 +73,13 @@ def build(verbose: bool = False, force: bool = False) -> str:
                 sys.stderr.write(f.read())
         if rc != 0:
             failed.append(src)
+            continue
+        with open(os.path.join(CSRC, src)) as f, open(log.name) as g:
+            try:
+                check_registers(src, f.read(), g.read())
+            except RuntimeError as e:
+                os.remove(os.path.join(BUILD, src + ".o"))  # not to be linked by the next build
+                failed.append(str(e))
     if failed:
         raise RuntimeError(f"nvcc failed for {failed}; logs in {BUILD}")
     if force or jobs or _stale(LIB, objs):

@@ -1226,7 +1226,8 @@ int launch(const Maps &maps, const Args &a, cudaStream_t s, const DevInfo &dev) 
   std::call_once(once[dev.device], [&] {
     err[dev.device] = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::Smem);
     cudaFuncAttributes fa;
-    // The helpers' registers go to the others out of what a block is launched with: it has to be all of it.
+    // The helpers' registers go to the others out of what a block is launched with: it has to be all of it (the build
+    // checks that as well).
     if (err[dev.device] == cudaSuccess) err[dev.device] = cudaFuncGetAttributes(&fa, kern);
     if (err[dev.device] == cudaSuccess && fa.numRegs != kLaunchRegs) err[dev.device] = cudaErrorInvalidValue;
   });
