@@ -359,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 
     const float f = fac[g];
 
-    // Weights are p = 2^(score - m), at most 2^kTop. m is the unit's own largest score, so that a unit's weights keep
-    // their bits after a token that had far more weight; it changes by whole powers of two, which are exact.
+    // Weights are p = 2^(score - m) times 2^kTop. m is the unit's own largest score, rounded up, so that a unit's weights
+    // keep their bits after a token that had far more weight; it changes by whole powers of two, which are exact.
     float m = -INFINITY;
     float highest = -INFINITY;  // the largest m so far: m is at most 2^kFall below it, which keeps sums finite
     float l = 0;                // this lane's sum of p
@@ -466,8 +466,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
         // scores that are all NaN or -infinity gives NaN, as the formula does.
         mx *= f;  // a power of two: exact
         if (pages_ok) mx = fmaxf(mx, -3.402823466e38f);
-        // rounded up: the largest weight is never above 2^kTop
-        const float own = __fadd_ru(ceilf(mx), -static_cast<float>(kTop));
+        const float own = ceilf(mx);
         highest = fmaxf(highest, own);
         const float m2 = fmaxf(own, highest - static_cast<float>(kFall));
         const float ref = m2 == -INFINITY ? 0.0f : -m2;
@@ -481,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) kv4_attn_kernel(const 
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const float2 y = __ffma2_rn(s[h][i], make_float2(f, f), make_float2(ref, ref));
-            s[h][i] = make_float2(ex2(y.x), ex2(y.y));
+            // times 2^kTop only here: an exponent of up to 14 would round at 2^-21
+            s[h][i] = __fmul2_rn(make_float2(ex2(y.x), ex2(y.y)), make_float2(1 << kTop, 1 << kTop));
           }
         const float2 sum = __fadd2_rn(__fadd2_rn(s[0][0], s[0][1]), __fadd2_rn(s[1][0], s[1][1]));
         l += sum.x + sum.y;
