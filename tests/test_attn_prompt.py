@@ -461,3 +461,19 @@ def test_ends_out_of_order_leave_the_sequences_beside_them_right(dtype):
     want, tol = exact(q, k, v, [100, 300], 0.125)
     assert ((out.double() - want).abs() <= tol)[100:192].all()  # whole tiles of 64 rows before the shared ones
     assert woq.device_status() == _lib.WOQ_OK
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_tiny_rows_of_very_different_sizes(dim):
+    """float32: values of 1e-27 and less in tiles with a power for each row, behind a tile with nearly all the weight."""
+    cu = [0, 300]
+    q, k, v = fused(23, 300, 4, 2, dim, torch.float32)
+    g = torch.Generator().manual_seed(4)
+    sizes = torch.exp2(torch.randint(-15, 1, (300, 1, 1), generator=g).float()).cuda() * 1e-27
+    q, k2 = q.abs() + 0.1, k * 0.1
+    k2[:20] = 2.0 * (dim / 64) ** -0.5  # scores of 16 and more above the others
+    v2 = v * sizes
+    v2[:20] = v[:20] * 1e-33
+    out = woq.attn_prompt(q, k2, v2, ints(cu)).double()
+    want, tol = exact(q, k2, v2, cu, dim**-0.5)
+    assert ((out - want).abs() <= tol).all()

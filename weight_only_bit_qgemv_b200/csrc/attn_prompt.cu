@@ -842,9 +842,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) ptx::mbar_arrive(&sh.p_full[t][(count + j + 1) & 1]);
         };
-        // A tile whose rows have powers of two of their own, or whose scores may be far from zero (it is rare): its scores become, in their place, the
-        // logarithms of the weights times their values' powers, less the largest, so that the tile's own code finds
-        // weights of at most 2^13. What they are to be multiplied with, the maximum and the sum are made here.
+        // A tile whose rows have powers of two of their own, or whose scores may be far from zero (it is rare): its scores
+        // become, in their place, the logarithms of the weights times their values' powers, less the largest, so that
+        // the tile's own code finds weights of at most 2^13. What they are to be multiplied with, the maximum and the
+        // sum are made here.
         struct Own {
           float m, l, alpha, v_pow;
         };
@@ -862,11 +863,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               ptx::tmem_ld_wait(x);
 #pragma unroll
               for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(f(__uint_as_float(x[i]), ch + i));
+              __syncwarp();
               ptx::tmem_st_32x32b_x16(s_addr + ch, x);
             }
             ptx::tmem_st_wait();
           };
-          float top = -3.402823466e38f, high = top;  // finite, also where all scores are -infinity or NaN
+          float top = -3.402823466e38f;  // finite, also where all scores are -infinity or NaN
+          float high = -120;             // what they are multiplied with is a normal number
           each([&](float x, int i) {
             x = i > lim ? -INFINITY : x * (scale * (k_pow < 0 ? __ldg(kr + min(i, last)) : k_pow));
             top = fmaxf(top, x);
@@ -879,7 +882,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           each([&](float x, int i) {
             x -= own.m;
             own.l += ex2(x + kWeightBits);
-            if (i <= lim) x += ilogbf(v_pow < 0 ? __ldg(vr + min(i, last)) : v_pow);
+            const float v = i > lim ? 1.0f : v_pow < 0 ? __ldg(vr + min(i, last)) : v_pow;  // a power of two
+            x += static_cast<int>(__float_as_uint(v) >> 23) - 127;
             high = fmaxf(high, x);
             return x;
           });
