@@ -477,3 +477,20 @@ def test_tiny_rows_of_very_different_sizes(dim):
     out = woq.attn_prompt(q, k2, v2, ints(cu)).double()
     want, tol = exact(q, k2, v2, cu, dim**-0.5)
     assert ((out - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("size", [2.0**13, 0.999 * 2.0**15, 1.001 * 2.0**15, 2.0**16, 2.0**18])
+def test_equal_scores_about_where_they_count_as_far_from_zero(dtype, sign, size):
+    """All products at the upper end of their powers of two: scores of 506 `size` to base 2, all the same."""
+    q = torch.full((200, 2, 128), 1.9921875, dtype=dtype, device="cuda")
+    k = sign * q[:, :1].contiguous()
+    v = torch.randn(200, 1, 128, generator=torch.Generator().manual_seed(5)).to(dtype).cuda()
+    out = woq.attn_prompt(q, k, v, ints([0, 70, 200]), scale=size / 1.4426950408889634).double()
+    unit = 0.0 if dtype == torch.float32 else ref.UNIT[dtype]
+    for a, b in ((0, 70), (70, 200)):
+        count = torch.arange(1, b - a + 1, device="cuda", dtype=torch.float64)[:, None]
+        want, col = (x.double().cumsum(0) / count for x in (v[a:b, 0], v[a:b, 0].abs()))
+        tol = (2.0**-18 + 2 * unit) * col + unit * want.abs()
+        assert ((out[a:b] - want[:, None]).abs() <= tol[:, None]).all()

@@ -58,10 +58,10 @@ constexpr int kSplitRows = 64;           // rows of a float32 tile of keys or va
 constexpr float kLag = 8;                // what 16-bit rows' weights may exceed 1 by, as a power of two
 constexpr int kWeightBits = 13;          // float32 rows' weights reach 2^kWeightBits
 constexpr int kSpread = 10;              // one power of two for them, if their sizes lie within 2^kSpread of one another
-// A score's factor from which on float32 rows' scores may reach 2^23: they are sums of 128 products below 2^28. Above
+// A score's factor from which on float32 rows' scores may reach 2^24: they are sums of 128 products below 2^28. Above
 // that, `largest less itself` in one fused step would be what its product was rounded by, and from 2^26 on a weight of
 // that leaves binary16.
-constexpr float kFar = 0x1p-12f;
+constexpr float kFar = 0x1p-11f;
 constexpr int kThreads = 384;
 constexpr int kLaunchRegs = 168;
 constexpr uint32_t kTmemCols = 512;
@@ -819,7 +819,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float scale = a.scale;
         const int64_t pow0 = static_cast<int64_t>(kv_head) * a.tiles;
         const int tile0 = sh.item[it & 1].tile0;
-        if (row < len) scale *= a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row];
+        // rows behind the sequence are another's, or none: no scores of theirs make a tile rare
+        scale = row < len ? scale * a.q_pow[static_cast<int64_t>(head) * a.tokens + start + row] : 0.0f;
         // o = o alpha + a tile's product
         auto accumulate = [&](int j, float alpha, float v_pow) {
           if (!wait(&sh.t_full[t], (count + j) & 1)) return;
