@@ -1,5 +1,5 @@
 // The 4-bit cache's layout and the helpers that its kernels and the prompt attention share:
-// element types, the sequence a packed row belongs to, and the page a cached token is in.
+// element types, the softmax's exponential, and the sequence that a packed row belongs to.
 //
 // codes  [pages, kv_heads, 2 (key, value), page, dim / 2] bytes
 // scales [pages, kv_heads, page, 2 (key, value), dim / 32] binary16
@@ -19,6 +19,13 @@
 #include "woq.h"
 
 namespace woq {
+
+// 2^x, within 2^-22 of it; below 2^-126 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 // Four consecutive elements of one row, as float.
 __device__ __forceinline__ float4 load4(const void *base, int64_t at, int dtype) {
