@@ -35,9 +35,9 @@
 // every masked pair of the block, so their values are looked at, what is not finite is replaced by 0 in shared memory,
 // and added after the last tile to the rows that do see it.
 //
-// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20 us, 4096 233 us (26 of them the
-// planes; 1 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 705 us (130 the planes); 32,768
-// bfloat16 tokens 3.9 ms, 1.13 PFLOP/s.
+// Measured (16 query heads on 8 key heads, dim 128): 137 float32 tokens 20 us, 4096 235 us (26 of them the
+// planes; 1 PFLOP/s of products in the rest), 24 prompts of 11 to 2011 710 us (130 the planes); 32,768
+// bfloat16 tokens 3.9 ms, 1.12 PFLOP/s. The power cap holds the clock of the long ones at 1537 to 1747 MHz.
 #include <algorithm>
 #include <mutex>
 #include <type_traits>

@@ -32,9 +32,10 @@
 // (three per 16 tokens: keys, values, scales are each contiguous within a page). Three blocks of four warps with
 // two units each under way keep 110 KB an SM in flight; more blocks or stages gained nothing.
 //
-// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 131 us
-// (2.3 TB/s), 4 of 100,000 to 131,072 174 us (3.1 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 69 us.
-// What holds it back is not the bytes but 27 instructions a token and key head, issued in 53 % of the
+// Measured (8 key heads, dim 128): 1 x 1000 tokens 9.9 us, 64 sequences of 1 to 8191 130 us
+// (2.3 TB/s), 4 of 100,000 to 131,072 175 us (3.0 TB/s), 16 of 2049 to 16,001 with 8 query heads a key head 70 us; FP32
+// products in every unit are 23 % slower.
+// What holds it back is not the bytes but 27 instructions a token and key head, issued in 54 % of the
 // cycles: three warps a scheduler, whose registers are full, do not cover one another's latencies better.
 #include <algorithm>
 #include <mutex>
